@@ -6,6 +6,10 @@ pass raw device pointers and the current HIP stream to the library, and
 return the output tensor. Every arithmetic step runs in the library's HIP
 kernels; PyTorch provides device memory and streams only.
 
+The serving operators (the paged cache, attention with a shared prefix, 8-bit
+float products) take torch's float16, bfloat16, float32 and float8_e4m3fn
+tensors of the shapes given at each function.
+
 Weight tensors are flat ``torch.uint8`` device tensors (or 2-D, rows of
 packed blocks) holding the llama.cpp block bytes described in ``lqmm.h``.
 
@@ -24,6 +28,8 @@ __all__ = [
     "lqmm_gemv_i4g32",
     "lqmm_gemm_q4_0_f16", "lqmm_gemm_q4_k_f16",
     "lqmm_gemv_workspace_bytes", "lqmm_status_string", "lqmm_version",
+    "lqmm_rope_turns", "lqmm_kv_append", "lqmm_attn_prefix", "lqmm_attn_prefix_workspace_bytes",
+    "lqmm_gemm_f8b128", "lqmm_quant_f8b128", "kv_cache_empty",
     "Q4_0_BLOCK_BYTES", "Q8_0_BLOCK_BYTES", "Q4_K_BLOCK_BYTES", "Q6_K_BLOCK_BYTES",
     "Q2_K_BLOCK_BYTES", "Q1_0_BLOCK_BYTES",
 ]
@@ -43,7 +49,9 @@ _lib = None
 EXPORTS = ("lqmm_sgemm", "lqmm_gemv_q4_0", "lqmm_gemv_q4_0_noalloc", "lqmm_gemm_q8_0_f16",
            "lqmm_gemv_q4_k", "lqmm_gemv_q8_0", "lqmm_gemv_q6_k", "lqmm_gemv_q2_k",
            "lqmm_gemv_q1_0", "lqmm_gemv_i4g32", "lqmm_gemm_q4_0_f16", "lqmm_gemm_q4_k_f16",
-           "lqmm_gemv_workspace_bytes", "lqmm_status_string", "lqmm_version")
+           "lqmm_gemv_workspace_bytes", "lqmm_status_string", "lqmm_version",
+           "lqmm_rope_turns", "lqmm_kv_append", "lqmm_attn_prefix",
+           "lqmm_attn_prefix_workspace_bytes", "lqmm_gemm_f8b128", "lqmm_quant_f8b128")
 
 
 class LqmmError(RuntimeError):
@@ -87,6 +95,19 @@ def load():
     lib.lqmm_gemm_q8_0_f16.restype = st
     lib.lqmm_gemv_workspace_bytes.argtypes = [i64, i64, i64]
     lib.lqmm_gemv_workspace_bytes.restype = sz
+    ci, f32 = ctypes.c_int, ctypes.c_float
+    lib.lqmm_rope_turns.argtypes = [p, i64, p]
+    lib.lqmm_kv_append.argtypes = ([p, p, p, ci] + [i64] * 3 + [p, p, p, i64, ci, p, p, p, ci]
+                                   + [i64] * 6 + [p])
+    lib.lqmm_attn_prefix.argtypes = [p, i64, p, p, ci, p, i64, p, i64, p, p, i64, p, p, f32,
+                                     *[i64] * 7, p, sz, p]
+    lib.lqmm_attn_prefix_workspace_bytes.argtypes = [i64] * 9
+    lib.lqmm_attn_prefix_workspace_bytes.restype = sz
+    lib.lqmm_gemm_f8b128.argtypes = [p, p, p, p, p, ci, i64, i64, i64, p]
+    lib.lqmm_quant_f8b128.argtypes = [p, ci, i64, p, p, i64, i64, p]
+    for name in ("lqmm_rope_turns", "lqmm_kv_append", "lqmm_attn_prefix", "lqmm_gemm_f8b128",
+                 "lqmm_quant_f8b128"):
+        getattr(lib, name).restype = st
     lib.lqmm_status_string.argtypes = [ctypes.c_int]
     lib.lqmm_status_string.restype = ctypes.c_char_p
     lib.lqmm_version.argtypes = []
@@ -363,3 +384,290 @@ def lqmm_gemv_i4g32(Wq, scales, zeros, x, N, out=None, workspace=None, stream=No
                                       x2.data_ptr(), out.data_ptr(), N, K, batch, ws_ptr,
                                       ws_bytes, st))
     return out.view(-1) if squeeze and out.dim() == 2 and out.shape[0] == 1 else out
+
+
+# ---- serving operators ---------------------------------------------------------
+
+def _type_code(dtype, name, allowed):
+    """lqmm_type value of a torch dtype."""
+    torch = _torch()
+    code = {torch.float32: 0, torch.float16: 1, torch.bfloat16: 2}.get(dtype)
+    if code is None or code not in allowed:
+        raise TypeError(f"{name} has element type {dtype}, which this call does not take")
+    return code
+
+
+def _rows(t, heads, dim, name):
+    """(tokens, heads, dim) with contiguous rows: its row stride in elements."""
+    torch = _torch()
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.device.type != "cuda":
+        raise ValueError(f"{name} must be a device tensor")
+    if t.dim() != 3 or t.shape[1] != heads or t.shape[2] != dim:
+        raise ValueError(f"{name} must be (tokens, {heads}, {dim}), got {tuple(t.shape)}")
+    s = t.stride()
+    if s[2] != 1 or (heads > 1 and s[1] != dim):
+        raise ValueError(f"the heads of one token of {name} must be contiguous")
+    return s[0] if t.shape[0] > 1 else heads * dim
+
+
+def _cache(k_cache, v_cache):
+    """Checks the two caches; (num_pages, n_kv_heads, page_size, head_dim, type)."""
+    torch = _torch()
+    for t, name in ((k_cache, "k_cache"), (v_cache, "v_cache")):
+        if not isinstance(t, torch.Tensor):
+            raise TypeError(f"{name} must be a torch.Tensor")
+        _dev_tensor(t, t.dtype, name)
+    if k_cache.dim() != 4:
+        raise ValueError("k_cache must be (num_pages, n_kv_heads, page_size, head_dim)")
+    pages, hkv, ps, d = k_cache.shape
+    if ps % 8 or tuple(v_cache.shape) != (pages, hkv, ps // 8, d, 8):
+        raise ValueError("v_cache must be (num_pages, n_kv_heads, page_size / 8, head_dim, 8)")
+    if v_cache.dtype != k_cache.dtype:
+        raise TypeError("k_cache and v_cache differ in element type")
+    return pages, hkv, ps, d, _type_code(k_cache.dtype, "k_cache", (1, 2))
+
+
+def kv_cache_empty(num_pages, n_kv_heads, page_size, head_dim, dtype=None, device="cuda"):
+    """Uninitialized (k_cache, v_cache) in the library's page layout."""
+    torch = _torch()
+    if page_size % 8:
+        raise ValueError("page_size must be a multiple of 8")
+    dtype = dtype or torch.float16
+    k = torch.empty((num_pages, n_kv_heads, page_size, head_dim), dtype=dtype, device=device)
+    v = torch.empty((num_pages, n_kv_heads, page_size // 8, head_dim, 8), dtype=dtype, device=device)
+    return k, v
+
+
+def lqmm_rope_turns(inv_freq, device="cuda"):
+    """The rotation table of lqmm_kv_append: inv_freq (radians per position, any
+    sequence or host array) as 64-bit fractions of a turn, an int64 tensor on
+    ``device``. Make it once."""
+    import numpy as np
+    torch = _torch()
+    f = np.ascontiguousarray(np.asarray(inv_freq, dtype=np.float64).reshape(-1))
+    out = np.empty(f.shape, dtype=np.uint64)
+    _check(load().lqmm_rope_turns(f.ctypes.data, f.size, out.ctypes.data))
+    return torch.from_numpy(out.view(np.int64)).to(device)
+
+
+def lqmm_kv_append(q, k, v, positions, slots, k_cache, v_cache, rope_turns=None,
+                   interleaved=False, q_out=None, stream=None):
+    """Rotate q (tokens, n_q_heads, head_dim) and k by their positions and append
+    k, v (tokens, n_kv_heads, head_dim; float32, float16 or bfloat16, rows may
+    be strided) to the caches at ``slots`` (int64; negative: not appended).
+    Returns the rotated q in the caches' type (q may be None: returns None).
+    positions: int32; rope_turns: the table of lqmm_rope_turns, None rotates
+    nothing."""
+    torch = _torch()
+    pages, hkv, ps, d, ctype = _cache(k_cache, v_cache)
+    ldk, ldv = _rows(k, hkv, d, "k"), _rows(v, hkv, d, "v")
+    tokens = k.shape[0]
+    itype = _type_code(k.dtype, "k", (0, 1, 2))
+    if v.dtype != k.dtype or v.shape[0] != tokens:
+        raise ValueError("k and v must have the same element type and tokens")
+    _dev_tensor(slots, torch.int64, "slots")
+    devs = [k, v, slots, k_cache, v_cache]
+    rot, pos_ptr, turns_ptr = 0, None, None
+    if rope_turns is not None:
+        _dev_tensor(rope_turns, torch.int64, "rope_turns")
+        _dev_tensor(positions, torch.int32, "positions")
+        if positions.numel() != tokens:
+            raise ValueError(f"positions must have {tokens} entries")
+        rot, pos_ptr, turns_ptr = 2 * rope_turns.numel(), positions.data_ptr(), rope_turns.data_ptr()
+        devs += [rope_turns, positions]
+    if slots.numel() != tokens:
+        raise ValueError(f"slots must have {tokens} entries")
+    hq, ldq, q_ptr, out_ptr = 0, 0, None, None
+    if q is not None:
+        if not isinstance(q, torch.Tensor) or q.dim() != 3:
+            raise ValueError("q must be (tokens, n_q_heads, head_dim)")
+        hq = q.shape[1]
+        ldq = _rows(q, hq, d, "q")
+        if q.dtype != k.dtype or q.shape[0] != tokens:
+            raise ValueError("q and k must have the same element type and tokens")
+        if q_out is None:
+            q_out = torch.empty((tokens, hq, d), dtype=k_cache.dtype, device=k_cache.device)
+        _dev_tensor(q_out, k_cache.dtype, "q_out")
+        if tuple(q_out.shape) != (tokens, hq, d):
+            raise ValueError("q_out has the wrong shape")
+        q_ptr, out_ptr = q.data_ptr(), q_out.data_ptr()
+        devs += [q, q_out]
+    elif q_out is not None:
+        raise ValueError("q_out without q")
+    dev = _same_device(*devs)
+    with torch.cuda.device(dev):
+        _check(load().lqmm_kv_append(q_ptr, k.data_ptr(), v.data_ptr(), itype, ldq, ldk, ldv,
+                                     pos_ptr, slots.data_ptr(), turns_ptr, rot, int(interleaved),
+                                     out_ptr, k_cache.data_ptr(), v_cache.data_ptr(), ctype, tokens,
+                                     hq, hkv, d, ps, pages, _stream(stream)))
+    return q_out
+
+
+def lqmm_attn_prefix_workspace_bytes(prefix_len, max_pages, max_q, tokens, batch, n_q_heads,
+                                     n_kv_heads, head_dim, page_size) -> int:
+    return load().lqmm_attn_prefix_workspace_bytes(
+        int(prefix_len), int(max_pages), int(max_q), int(tokens), int(batch), int(n_q_heads),
+        int(n_kv_heads), int(head_dim), int(page_size))
+
+
+# Scratch for partial results when the caller passes no workspace: one buffer
+# per (device, stream), at least doubled when it grows. A buffer that was
+# outgrown is kept (they add up to less than the newest): launches in flight
+# and captured graphs may still use it.
+_scratch = {}
+
+
+def _scratch_for(device, stream_handle, nbytes):
+    torch = _torch()
+    bufs = _scratch.setdefault((device.index, int(stream_handle or 0)), [])
+    if not bufs or bufs[-1].numel() < nbytes:
+        grown = max(nbytes, 2 * bufs[-1].numel() if bufs else 1 << 20)
+        bufs.append(torch.empty(grown, dtype=torch.uint8, device=device))
+    return bufs[-1]
+
+
+def lqmm_attn_prefix(q, k_cache, v_cache, pages, seq_lens, prefix_pages=None, prefix_len=0,
+                     q_start=None, max_q=1, scale=None, out=None, return_lse=False, lse=None,
+                     workspace=None, stream=None):
+    """Attention of q (tokens, n_q_heads, head_dim) over the paged cache: every
+    sequence sees the first ``prefix_len`` tokens of ``prefix_pages`` (int32)
+    and then its own seq_lens[b] (int32) tokens in pages[b] (int32, (batch,
+    max_pages)), causally among its new tokens. One token per sequence, or
+    rows q_start[b] .. q_start[b + 1] - 1 (int32, batch + 1 entries) with at
+    most ``max_q`` of them. scale: 1 / sqrt(head_dim) when None. Returns out
+    (tokens, n_q_heads, head_dim), or (out, lse) with lse (tokens, n_q_heads)
+    float32 when return_lse is set or lse is given."""
+    torch = _torch()
+    npages, hkv, ps, d, ctype = _cache(k_cache, v_cache)
+    if not isinstance(q, torch.Tensor) or q.dim() != 3:
+        raise ValueError("q must be (tokens, n_q_heads, head_dim)")
+    tokens, hq = q.shape[0], q.shape[1]
+    ldq = _rows(q, hq, d, "q")
+    if q.dtype != k_cache.dtype:
+        raise TypeError("q must have the caches' element type")
+    _dev_tensor(pages, torch.int32, "pages")
+    _dev_tensor(seq_lens, torch.int32, "seq_lens")
+    if pages.dim() != 2 or seq_lens.dim() != 1 or pages.shape[0] != seq_lens.shape[0]:
+        raise ValueError("pages must be (batch, max_pages) and seq_lens (batch,)")
+    batch, max_pages = pages.shape
+    devs = [q, k_cache, v_cache, pages, seq_lens]
+    start_ptr = prefix_ptr = lse_ptr = None
+    if q_start is not None:
+        _dev_tensor(q_start, torch.int32, "q_start")
+        if q_start.numel() != batch + 1:
+            raise ValueError(f"q_start must have {batch + 1} entries")
+        start_ptr = q_start.data_ptr()
+        devs.append(q_start)
+    prefix_len = int(prefix_len)
+    if prefix_len:
+        _dev_tensor(prefix_pages, torch.int32, "prefix_pages")
+        if prefix_pages.numel() * ps < prefix_len:
+            raise ValueError("prefix_pages hold fewer than prefix_len tokens")
+        prefix_ptr = prefix_pages.data_ptr()
+        devs.append(prefix_pages)
+    if out is None:
+        out = torch.empty((tokens, hq, d), dtype=q.dtype, device=q.device)
+    _dev_tensor(out, q.dtype, "out")
+    if tuple(out.shape) != (tokens, hq, d):
+        raise ValueError("out has the wrong shape")
+    devs.append(out)
+    if return_lse and lse is None:
+        lse = torch.empty((tokens, hq), dtype=torch.float32, device=q.device)
+    if lse is not None:
+        _dev_tensor(lse, torch.float32, "lse")
+        if lse.numel() != tokens * hq:
+            raise ValueError("lse has the wrong size")
+        lse_ptr = lse.data_ptr()
+        devs.append(lse)
+    if scale is None:
+        scale = d ** -0.5
+    lib = load()
+    dev = _same_device(*devs)
+    with torch.cuda.device(dev):
+        st = _stream(stream)
+        need = lib.lqmm_attn_prefix_workspace_bytes(prefix_len, max_pages, max_q, tokens, batch, hq,
+                                                    hkv, d, ps)
+        ws_ptr, ws_bytes = None, 0
+        if workspace is None and need:
+            workspace = _scratch_for(dev, st, need)
+        if workspace is not None:
+            _dev_tensor(workspace, torch.uint8, "workspace")
+            ws_ptr, ws_bytes = workspace.data_ptr(), workspace.numel()
+        _check(lib.lqmm_attn_prefix(q.data_ptr(), ldq, k_cache.data_ptr(), v_cache.data_ptr(), ctype,
+                                    prefix_ptr, prefix_len, pages.data_ptr(), max_pages,
+                                    seq_lens.data_ptr(), start_ptr, max_q, out.data_ptr(), lse_ptr,
+                                    scale, tokens, batch, hq, hkv, d, ps, npages, ws_ptr, ws_bytes,
+                                    st))
+    return (out, lse) if lse is not None else out
+
+
+def _codes(t, name):
+    """A 2-D contiguous tensor of e4m3 codes (float8_e4m3fn or raw uint8)."""
+    torch = _torch()
+    if not isinstance(t, torch.Tensor) or t.dtype not in (torch.float8_e4m3fn, torch.uint8):
+        raise TypeError(f"{name} must be a float8_e4m3fn (or uint8) torch.Tensor")
+    _dev_tensor(t, t.dtype, name)
+    if t.dim() != 2:
+        raise ValueError(f"{name} must be 2-D")
+    return t
+
+
+def lqmm_quant_f8b128(X, out=None, scales=None, stream=None):
+    """X (M, K) float32, float16 or bfloat16 (rows may be strided) to e4m3 codes
+    with a scale per row and 128 columns: (codes (M, K) float8_e4m3fn, scales
+    (ceil(K / 128), M) float32)."""
+    torch = _torch()
+    if not isinstance(X, torch.Tensor) or X.dim() != 2:
+        raise ValueError("X must be (M, K)")
+    if X.device.type != "cuda":
+        raise ValueError("X must be a device tensor")
+    M, K = X.shape
+    if K > 1 and X.stride(1) != 1:
+        raise ValueError("the rows of X must be contiguous")
+    xtype = _type_code(X.dtype, "X", (0, 1, 2))
+    blocks = (K + 127) // 128
+    if out is None:
+        out = torch.empty((M, K), dtype=torch.float8_e4m3fn, device=X.device)
+    if scales is None:
+        scales = torch.empty((blocks, M), dtype=torch.float32, device=X.device)
+    _codes(out, "out")
+    _dev_tensor(scales, torch.float32, "scales")
+    if tuple(out.shape) != (M, K) or tuple(scales.shape) != (blocks, M):
+        raise ValueError("out or scales has the wrong shape")
+    dev = _same_device(X, out, scales)
+    with torch.cuda.device(dev):
+        _check(load().lqmm_quant_f8b128(X.data_ptr(), xtype, X.stride(0) if M > 1 else K,
+                                        out.data_ptr(), scales.data_ptr(), M, K, _stream(stream)))
+    return out, scales
+
+
+def lqmm_gemm_f8b128(W, wscale, Xq, xscale, out=None, out_dtype=None, stream=None):
+    """Y (M, N) = X @ W^T over e4m3 codes with a scale per block of 128: W (N, K)
+    with wscale (ceil(N / 128), ceil(K / 128)), Xq (M, K) with xscale
+    (ceil(K / 128), M) as lqmm_quant_f8b128 makes them. out_dtype: float16
+    (default), bfloat16 or float32."""
+    torch = _torch()
+    _codes(W, "W")
+    _codes(Xq, "Xq")
+    _dev_tensor(wscale, torch.float32, "wscale")
+    _dev_tensor(xscale, torch.float32, "xscale")
+    (N, K), M = W.shape, Xq.shape[0]
+    if Xq.shape[1] != K:
+        raise ValueError(f"shape mismatch: W {tuple(W.shape)} Xq {tuple(Xq.shape)}")
+    blocks = (K + 127) // 128
+    if tuple(wscale.shape) != ((N + 127) // 128, blocks) or tuple(xscale.shape) != (blocks, M):
+        raise ValueError("wscale or xscale has the wrong shape")
+    if out is None:
+        out = torch.empty((M, N), dtype=out_dtype or torch.float16, device=W.device)
+    ytype = _type_code(out.dtype, "out", (0, 1, 2))
+    _dev_tensor(out, out_dtype or out.dtype, "out")
+    if tuple(out.shape) != (M, N):
+        raise ValueError("out has the wrong shape")
+    dev = _same_device(W, wscale, Xq, xscale, out)
+    with torch.cuda.device(dev):
+        _check(load().lqmm_gemm_f8b128(W.data_ptr(), wscale.data_ptr(), Xq.data_ptr(),
+                                       xscale.data_ptr(), out.data_ptr(), ytype, M, N, K,
+                                       _stream(stream)))
+    return out

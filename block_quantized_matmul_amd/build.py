@@ -19,7 +19,8 @@ CSRC = os.path.join(HERE, "csrc")
 OBJ = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "liblqmm.so")
 SOURCES = ["api.hip", "gemv.hip", "gemv_small.hip", "gemv_small_more.hip", "gemm_q8_0.hip",
-           "gemm_lds.hip", "sgemm.hip", "gemv_whole.hip"]
+           "gemm_lds.hip", "sgemm.hip", "gemv_whole.hip", "api_serve.hip", "kv_append.hip",
+           "attn_prefix.hip", "f8b128.hip"]
 PROBE_LIB = os.path.join(HERE, "liblqmm_probe.so")
 PROBE_SOURCES = ["probe.hip"]
 

@@ -548,6 +548,8 @@ lqmm_status gemv_more(lqmm::GemvFormat f, int blk, const void *W, const float *a
 
 }  // namespace
 
+bool lqmm::device_cus(int *num_cus) { return current_device(num_cus) == LQMM_OK; }
+
 extern "C" {
 
 lqmm_status lqmm_sgemm(const float *A, const float *B, float *C, int64_t M, int64_t N, int64_t K,
@@ -678,6 +680,7 @@ const char *lqmm_status_string(int s) {
     case LQMM_ERR_WORKSPACE: return "LQMM_ERR_WORKSPACE: the call needs a larger workspace";
     case LQMM_ERR_DEVICE: return "LQMM_ERR_DEVICE: no usable gfx950 device";
     case LQMM_ERR_LAUNCH: return "LQMM_ERR_LAUNCH: kernel launch failed";
+    case LQMM_ERR_TYPE: return "LQMM_ERR_TYPE: an element type that the call does not take";
   }
   return "LQMM: unknown status";
 }

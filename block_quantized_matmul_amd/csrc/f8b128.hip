@@ -1,0 +1,285 @@
+// Matrix products in 8-bit floating point (e4m3) with an fp32 scale for each
+// block of 128, and the quantization of activations to that form.
+//
+// Mathematics. W is N x K codes with one scale for each 128 x 128 block, X is
+// M x K codes with one scale for each row and group of 128 columns:
+//   Y[m][n] = sum_b sx[b][m] sw[n / 128][b] sum_{k in block b} X[m][k] W[n][k].
+// One v_mfma_f32_16x16x128_f8f6f4 is the inner sum of one scale block for a
+// 16 x 16 tile, started from zero; the outer sum is one fp32 multiply-add
+// with the product of the two scales.
+//
+// Which matrix cores. The f8 ones do not sum in fp32: a product is cut off
+// 14 bits below the largest of its group (measured: next to 448 * 448 =
+// 200704, products below 8 vanish and 9 counts as 8), a relative error of 1e-5
+// to 5e-5 of a sum. That is far below the rounding of a bf16 output (2^-8)
+// and not of the others, so bf16 products run on the f8 cores; for fp16 and
+// fp32 outputs the codes are turned into fp16 in registers (exactly) and
+// multiplied there, at half the rate, with fp32 sums.
+//
+// Layout. With W as the A operand, a lane holds
+// four outputs of one row m (m = lane & 15), so the scale product is one
+// value per lane and 16 rows of X: four multiply-adds per matrix
+// instruction, which run on the vector ALU beside it.
+#include "lqmm_internal.hpp"
+#include "serve_device.hpp"
+
+namespace lqmm {
+namespace {
+
+typedef int i32x8 __attribute__((ext_vector_type(8)));
+typedef int i32x4 __attribute__((ext_vector_type(4)));
+
+// ---- activations to e4m3 ----------------------------------------------------
+constexpr int kQuantThreads = 256;
+constexpr float kF8Max = 448.0f;
+
+// Largest value over aligned groups of 16 lanes, in every lane.
+__device__ __forceinline__ float max16(float v) {
+  v = fmaxf(v, dpp<0xB1>(v));   // quad_perm [1,0,3,2]
+  v = fmaxf(v, dpp<0x4E>(v));   // quad_perm [2,3,0,1]
+  v = fmaxf(v, dpp<0x141>(v));  // row_half_mirror
+  v = fmaxf(v, dpp<0x140>(v));  // row_mirror
+  return v;
+}
+
+// 16 lanes take one group of 128 (8 elements each); a workgroup takes 16
+// rows of one group, so that the codes are written in whole 128-byte lines
+// and the scales in 64-byte runs.
+template <class T>
+__global__ void __launch_bounds__(kQuantThreads)
+quant_f8b128_kernel(const typename T::elem *__restrict__ X, int64_t ldx, uint8_t *__restrict__ Xq,
+                    float *__restrict__ xs, int64_t M, int64_t K, int blocks) {
+  const int l16 = threadIdx.x & 15;
+  const int b = blockIdx.x % blocks;
+  const int64_t m = (int64_t)(blockIdx.x / blocks) * 16 + (threadIdx.x >> 4);
+  const int64_t k = (int64_t)b * 128 + 8 * l16;
+  if (m >= M) return;  // whole 16-lane groups
+  float x[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+  if (k < K) load8<T>(X + m * ldx + k, x);
+  float top = 0.f;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) top = fmaxf(top, fabsf(x[i]));
+  // 2^-126: a group of zeros keeps a finite scale
+  const float scale = fmaxf(max16(top) / kF8Max, 0x1p-126f);
+  if (k < K) {
+    uint32_t w[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      // IEEE divisions: the codes are those of x / scale, ties included
+      int v = __builtin_amdgcn_cvt_pk_fp8_f32(x[4 * i] / scale, x[4 * i + 1] / scale, 0, false);
+      v = __builtin_amdgcn_cvt_pk_fp8_f32(x[4 * i + 2] / scale, x[4 * i + 3] / scale, v, true);
+      w[i] = (uint32_t)v;
+    }
+    *reinterpret_cast<u32x2 *>(Xq + m * K + k) = u32x2{w[0], w[1]};
+  }
+  if (l16 == 0) xs[(int64_t)b * M + m] = scale;
+}
+
+// ---- product ----------------------------------------------------------------
+// Four consecutive outputs y[0..3] of one row, of which the first `n` exist.
+template <class T>
+__device__ __forceinline__ void store4(typename T::elem *p, float4_t v, int n, bool vec) {
+  typedef typename T::elem elem;
+  typedef elem vec4 __attribute__((ext_vector_type(4)));
+  const vec4 o = {(elem)v[0], (elem)v[1], (elem)v[2], (elem)v[3]};
+  if (vec && n >= 4) {
+    *reinterpret_cast<vec4 *>(p) = o;
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (i < n) p[i] = o[i];
+  }
+}
+
+constexpr int BK = 128;
+
+// 32 codes as four operands of the fp16 matrix cores (exact).
+__device__ __forceinline__ void to_f16(i32x8 c, half8_t (&h)[4]) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const half2_t a = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(c[2 * i], 1.0f, false);
+    const half2_t b = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(c[2 * i], 1.0f, true);
+    const half2_t d = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(c[2 * i + 1], 1.0f, false);
+    const half2_t e = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(c[2 * i + 1], 1.0f, true);
+    h[i] = half8_t{a[0], a[1], b[0], b[1], d[0], d[1], e[0], e[1]};
+  }
+}
+
+// A 16-row operand of one scale block, and the sum of one block's products.
+template <bool F8>
+struct Operand;
+template <>
+struct Operand<true> {
+  i32x8 v;
+  __device__ __forceinline__ void set(i32x8 c) { v = c; }
+};
+template <>
+struct Operand<false> {
+  half8_t v[4];
+  __device__ __forceinline__ void set(i32x8 c) { to_f16(c, v); }
+};
+__device__ __forceinline__ float4_t block_sum(const Operand<true> &a, const Operand<true> &b) {
+  return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a.v, b.v, float4_t{0.f, 0.f, 0.f, 0.f}, 0,
+                                                          0, 0, 0, 0, 0);
+}
+__device__ __forceinline__ float4_t block_sum(const Operand<false> &a, const Operand<false> &b) {
+  float4_t p = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) p = __builtin_amdgcn_mfma_f32_16x16x32_f16(a.v[i], b.v[i], p, 0, 0, 0);
+  return p;
+}
+
+// BM x BN tile (rows of X by rows of W), WM x WN waves.
+template <class T, int BM, int BN, int WM, int WN>
+__global__ void __launch_bounds__(64 * WM * WN)
+gemm_f8b128_kernel(const uint8_t *__restrict__ W, const float *__restrict__ sw,
+                   const uint8_t *__restrict__ X, const float *__restrict__ sx,
+                   typename T::elem *__restrict__ Y, int64_t M, int64_t N, int64_t K, int tiles_m) {
+  constexpr bool F8 = __is_same(T, TypeBF16);
+  constexpr int kWaves = WM * WN;
+  constexpr int TM = BM / WM / 16, TN = BN / WN / 16;  // 16 x 16 tiles of a wave
+  constexpr int kStage = (BM + BN) * BK;
+  constexpr int kLoads = (BM + BN) / 8 / kWaves;  // 1 KB loads of a wave per step
+  static_assert((BM + BN) / 8 % kWaves == 0 && BN / WN <= 128 && 128 % (BN / WN) == 0, "tile");
+  extern __shared__ __attribute__((aligned(16))) uint8_t smem[];
+
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int l16 = lane & 15, g = lane >> 4;
+  const int tile = blockIdx.x;
+  const int64_t m0 = (int64_t)(tile % tiles_m) * BM, n0 = (int64_t)(tile / tiles_m) * BN;
+  const int wm = (wave % WM) * (BM / WM), wn = (wave / WM) * (BN / WN);
+  const int blocks = (int)((K + BK - 1) / BK);
+  const uint32_t Ku = (uint32_t)K;
+
+  const int64_t xrows = M - m0 < BM ? M - m0 : BM;
+  const int64_t wrows = N - n0 < BN ? N - n0 : BN;
+  const rsrc_t xr = make_rsrc(X + m0 * K, (uint32_t)(xrows * K));
+  const rsrc_t wr = make_rsrc(W + n0 * K, (uint32_t)(wrows * K));
+
+  // Tile rows of 128 bytes; 16-byte chunk c of row r stands in slot
+  // c ^ (r & 7), so that the eight rows that one phase of a 16-byte LDS read
+  // touches lie in different banks. A load fills 8 rows, lane by lane.
+  const int lrow = lane >> 3, lcol = 16 * ((lane & 7) ^ lrow);
+  auto issue = [&](int kt) {
+    uint8_t *st = smem + (kt & 1) * kStage;
+    // past K the rows of the next line begin: those chunks read as zeros
+    // (an offset past the resource)
+    const bool in = (uint32_t)(kt * BK + lcol) < Ku;
+#pragma unroll
+    for (int i = 0; i < kLoads; ++i) {
+      const int j = wave * kLoads + i;  // 8 rows: X first, then W
+      const bool is_x = j < BM / 8;
+      const int r = 8 * (is_x ? j : j - BM / 8) + lrow;
+      const int off = in ? (int)((uint32_t)r * Ku + lcol) : (int)0x80000000u;
+      if (is_x)
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(xr, st + j * 1024, 16, off, kt * BK, 0, 0);
+      else
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(wr, st + j * 1024, 16, off, kt * BK, 0, 0);
+    }
+  };
+  auto frag = [&](const uint8_t *base, int row) {
+    const int s = row & 7;
+    const i32x4 lo = *reinterpret_cast<const i32x4 *>(base + row * BK + 16 * (g ^ s));
+    const i32x4 hi = *reinterpret_cast<const i32x4 *>(base + row * BK + 16 * ((g + 4) ^ s));
+    return __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
+  };
+
+  const int64_t nblk = (n0 + wn) / 128;
+  const bool n_in = n0 + wn < N;
+  float4_t acc[TM][TN];
+#pragma unroll
+  for (int i = 0; i < TM; ++i)
+#pragma unroll
+    for (int j = 0; j < TN; ++j) acc[i][j] = float4_t{0.f, 0.f, 0.f, 0.f};
+
+  issue(0);
+  for (int kt = 0; kt < blocks; ++kt) {
+    asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+    if (kt + 1 < blocks) issue(kt + 1);
+    const uint8_t *xst = smem + (kt & 1) * kStage, *wst = xst + BM * BK;
+    const float s_n = n_in ? sw[nblk * blocks + kt] : 0.f;
+    float s[TM];
+#pragma unroll
+    for (int i = 0; i < TM; ++i) {
+      const int64_t m = m0 + wm + 16 * i + l16;
+      s[i] = m < M ? sx[(int64_t)kt * M + m] * s_n : 0.f;
+    }
+    Operand<F8> wf[TN];
+#pragma unroll
+    for (int j = 0; j < TN; ++j) wf[j].set(frag(wst, wn + 16 * j + l16));
+#pragma unroll
+    for (int i = 0; i < TM; ++i) {
+      Operand<F8> xf;
+      xf.set(frag(xst, wm + 16 * i + l16));
+#pragma unroll
+      for (int j = 0; j < TN; ++j) {
+        const float4_t p = block_sum(wf[j], xf);
+#pragma unroll
+        for (int r = 0; r < 4; ++r) acc[i][j][r] += p[r] * s[i];
+      }
+    }
+  }
+
+  const bool vec = N % 4 == 0;
+#pragma unroll
+  for (int i = 0; i < TM; ++i) {
+    const int64_t m = m0 + wm + 16 * i + l16;
+    if (m >= M) continue;
+#pragma unroll
+    for (int j = 0; j < TN; ++j) {
+      const int64_t n = n0 + wn + 16 * j + 4 * g;
+      if (n < N) store4<T>(Y + m * N + n, acc[i][j], (int)(N - n < 4 ? N - n : 4), vec);
+    }
+  }
+}
+
+template <class T, int BM, int BN, int WM, int WN>
+hipError_t launch_tile(const uint8_t *W, const float *sw, const uint8_t *X, const float *sx, void *Y,
+                       int64_t M, int64_t N, int64_t K, hipStream_t stream) {
+  constexpr int kLds = 2 * (BM + BN) * BK;
+  constexpr auto kern = gemm_f8b128_kernel<T, BM, BN, WM, WN>;
+  const int64_t tm = (M + BM - 1) / BM, tn = (N + BN - 1) / BN;
+  if (tm * tn > 0x7fffffff) return hipErrorInvalidValue;
+  const hipError_t e = ensure_max_lds<kern>(kLds);
+  if (e != hipSuccess) return e;
+  hipLaunchKernelGGL(kern, dim3((unsigned)(tm * tn)), dim3(64 * WM * WN), kLds, stream, W, sw, X, sx,
+                     static_cast<typename T::elem *>(Y), M, N, K, (int)tm);
+  return hipGetLastError();
+}
+
+template <class T>
+hipError_t launch_gemm(const uint8_t *W, const float *sw, const uint8_t *X, const float *sx, void *Y,
+                       int64_t M, int64_t N, int64_t K, hipStream_t stream) {
+  return launch_tile<T, 128, 128, 2, 2>(W, sw, X, sx, Y, M, N, K, stream);
+}
+
+template <class T>
+hipError_t launch_quant(const void *X, int64_t ldx, uint8_t *Xq, float *xs, int64_t M, int64_t K,
+                        hipStream_t stream) {
+  const int64_t blocks = (K + 127) / 128, rows = (M + 15) / 16;
+  if (blocks * rows > 0x7fffffff) return hipErrorInvalidValue;
+  hipLaunchKernelGGL(quant_f8b128_kernel<T>, dim3((unsigned)(blocks * rows)), dim3(kQuantThreads), 0,
+                     stream, static_cast<const typename T::elem *>(X), ldx, Xq, xs, M, K, (int)blocks);
+  return hipGetLastError();
+}
+
+}  // namespace
+
+hipError_t quant_f8b128_launch(const void *X, ElemType type, int64_t ldx, uint8_t *Xq, float *xs,
+                               int64_t M, int64_t K, hipStream_t stream) {
+  if (type == ElemType::F32) return launch_quant<TypeF32>(X, ldx, Xq, xs, M, K, stream);
+  if (type == ElemType::F16) return launch_quant<TypeF16>(X, ldx, Xq, xs, M, K, stream);
+  return launch_quant<TypeBF16>(X, ldx, Xq, xs, M, K, stream);
+}
+
+hipError_t gemm_f8b128_launch(const uint8_t *W, const float *sw, const uint8_t *X, const float *sx,
+                              void *Y, ElemType type, int64_t M, int64_t N, int64_t K, int num_cus,
+                              hipStream_t stream) {
+  (void)num_cus;
+  if (type == ElemType::F32) return launch_gemm<TypeF32>(W, sw, X, sx, Y, M, N, K, stream);
+  if (type == ElemType::F16) return launch_gemm<TypeF16>(W, sw, X, sx, Y, M, N, K, stream);
+  return launch_gemm<TypeBF16>(W, sw, X, sx, Y, M, N, K, stream);
+}
+
+}  // namespace lqmm

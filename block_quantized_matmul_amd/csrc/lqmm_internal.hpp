@@ -144,4 +144,55 @@ hipError_t gemm_lds_launch(GemmFormat f, const uint8_t *W, const uint16_t *X, ui
 hipError_t sgemm_launch(const float *A, const float *B, float *C, int64_t M, int64_t N,
                         int64_t K, int num_cus, hipStream_t stream);
 
+// ---- serving operators --------------------------------------------------------
+// The current device's CU count, checked to be gfx950 (api.hip); false when
+// there is no such device.
+bool device_cus(int *num_cus);
+
+enum class ElemType { F32, F16, BF16 };
+
+// Keys and values into a paged cache with rotation (kv_append.hip). Strides
+// in elements; q and q_out are null with n_q_heads = 0 when there is no q.
+struct KvAppend {
+  const void *q, *k, *v;
+  const int32_t *positions;  // per token; null with rot_dim = 0
+  const int64_t *slots;      // per token: page * page_size + offset, < 0 = none
+  const uint64_t *turns;     // rot_dim / 2
+  void *q_out, *k_cache, *v_cache;
+  int64_t ldq, ldk, ldv, tokens, num_pages;
+  int n_q_heads, n_kv_heads, head_dim, rot_dim, interleaved, page_log2;
+  // set by the launch
+  int heads_per_block, head_blocks, rot_blocks;
+};
+hipError_t kv_append_launch(KvAppend a, ElemType in, ElemType cache, hipStream_t stream);
+
+// Attention over the cache with a shared prefix (attn_prefix.hip).
+constexpr int kAttnMaxChunk = 8192;  // keys of one work item
+struct AttnPrefix {
+  const void *q, *k_cache, *v_cache;
+  const int32_t *prefix_pages, *pages, *lens, *q_start;
+  void *out;
+  float *lse;
+  int64_t ldq, tokens, batch, max_q, num_pages, max_pages, prefix_len;
+  int n_q_heads, n_kv_heads, head_dim, page_log2;
+  float scale_log2;  // scale * log2(e)
+  // plan (attn_prefix_plan)
+  int group, prefix_row_blocks, prefix_chunk, prefix_parts;
+  int suffix_row_blocks, suffix_chunk, suffix_parts;
+  int64_t prefix_items, suffix_items;
+  float *part_o;    // parts x (tokens x heads) x head_dim
+  float2 *part_ml;  // parts x (tokens x heads): reference, sum
+};
+// Splits the work; reads the sizes, writes the plan.
+void attn_prefix_plan(AttnPrefix &a, int64_t max_suffix, int num_cus);
+size_t attn_prefix_workspace(const AttnPrefix &a);
+hipError_t attn_prefix_launch(AttnPrefix &a, void *ws, ElemType type, hipStream_t stream);
+
+// e4m3 codes with a scale per block of 128 (f8b128.hip).
+hipError_t quant_f8b128_launch(const void *X, ElemType type, int64_t ldx, uint8_t *Xq, float *xs,
+                               int64_t M, int64_t K, hipStream_t stream);
+hipError_t gemm_f8b128_launch(const uint8_t *W, const float *sw, const uint8_t *X, const float *sx,
+                              void *Y, ElemType type, int64_t M, int64_t N, int64_t K, int num_cus,
+                              hipStream_t stream);
+
 }  // namespace lqmm

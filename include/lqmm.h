@@ -86,7 +86,8 @@ typedef enum {
   LQMM_ERR_ALIGN = 3,     /* a pointer is not 16-byte aligned */
   LQMM_ERR_WORKSPACE = 4, /* the call needs a workspace (split-K partial sums) and got none or too small a one */
   LQMM_ERR_DEVICE = 5,    /* no usable HIP device, or it is not a gfx950 GPU */
-  LQMM_ERR_LAUNCH = 6     /* a kernel launch failed (hipGetLastError) */
+  LQMM_ERR_LAUNCH = 6,    /* a kernel launch failed (hipGetLastError) */
+  LQMM_ERR_TYPE = 7       /* an element type that the call does not take */
 } lqmm_status;
 
 /* Largest size accepted for any dimension (elements). */
@@ -236,6 +237,132 @@ lqmm_status lqmm_gemm_q4_0_f16(const void *W, const uint16_t *X, uint16_t *Y,
                                int64_t M, int64_t N, int64_t K, void *stream);
 lqmm_status lqmm_gemm_q4_k_f16(const void *W, const uint16_t *X, uint16_t *Y,
                                int64_t M, int64_t N, int64_t K, void *stream);
+
+/*
+ * ---- serving operators ------------------------------------------------------
+ * What a decoder layer runs between its weight products: keys and values into
+ * a paged cache, attention over that cache, and products with 8-bit float
+ * weights. Element types are passed as lqmm_type values (LQMM_ERR_TYPE for any
+ * other); row strides (ld*) are in elements and a multiple of 16 bytes
+ * (LQMM_ERR_ALIGN), the elements of one row (all heads of one token) are
+ * contiguous. Index arrays (positions, slots, page numbers, lengths, rope
+ * tables) and lse need only their element's alignment, all other pointers 16
+ * bytes.
+ */
+typedef enum { LQMM_F32 = 0, LQMM_F16 = 1, LQMM_BF16 = 2 } lqmm_type;
+
+/*
+ * The paged cache. Memory of num_pages pages of page_size tokens (a power of
+ * two, 8 .. 1024), fp16 or bf16, for n_kv_heads heads of head_dim (64, 96, 128
+ * or 256) elements:
+ *   k_cache [num_pages][n_kv_heads][page_size][head_dim]
+ *   v_cache [num_pages][n_kv_heads][page_size / 8][head_dim][8]
+ * In v_cache the eight tokens of an aligned group of eight are adjacent for
+ * each dimension (token o of a page is element o % 8 of group o / 8), which is
+ * the order that the matrix cores take. A token's slot is
+ * page * page_size + (its place in the page).
+ */
+
+/*
+ * Angles of the position rotation: turns[i] = inv_freq[i] / (2 pi) as a 64-bit
+ * fraction of a turn, for n frequencies. HOST pointers, host arithmetic; copy
+ * the table to the device once. position * turns[i] mod 2^64 is then the angle
+ * with its whole turns dropped, at any position. LQMM_ERR_SHAPE when a
+ * frequency is not finite.
+ */
+lqmm_status lqmm_rope_turns(const double *inv_freq, int64_t n, uint64_t *turns);
+
+/*
+ * Rotate q and k by their positions, append k and v to the cache.
+ * q: tokens x (n_q_heads * head_dim), row stride ldq; k, v: tokens x
+ * (n_kv_heads * head_dim), row strides ldk, ldv; all of in_type (fp32, fp16 or
+ * bf16; slices of one projection's output are such rows). q_out: tokens x
+ * n_q_heads x head_dim of cache_type (fp16 or bf16). q may be NULL, with
+ * n_q_heads 0: only k and v are appended. positions: one int32 per token.
+ * slots: one int64 per token; a token whose slot is negative or past the cache
+ * is not appended (its q is still rotated). Two tokens with the same slot
+ * leave either one there. rope_turns: rotary_dim / 2 entries; rotary_dim is a
+ * multiple of 16, at most head_dim, and 0 (with NULL positions and
+ * rope_turns) rotates nothing. Pair i of a head is elements (i, i +
+ * rotary_dim / 2), or (2i, 2i + 1) when `interleaved` is not 0; elements from
+ * rotary_dim on are copied. Computed in fp32, each result rounded once.
+ */
+lqmm_status lqmm_kv_append(const void *q, const void *k, const void *v, int in_type,
+                           int64_t ldq, int64_t ldk, int64_t ldv,
+                           const int32_t *positions, const int64_t *slots,
+                           const uint64_t *rope_turns, int64_t rotary_dim, int interleaved,
+                           void *q_out, void *k_cache, void *v_cache, int cache_type,
+                           int64_t tokens, int64_t n_q_heads, int64_t n_kv_heads,
+                           int64_t head_dim, int64_t page_size, int64_t num_pages,
+                           void *stream);
+
+/*
+ * Attention of a batch of sequences over the cache. Every sequence's keys are
+ * the prefix_len tokens of the shared pages prefix_pages (read once for all
+ * sequences; prefix_len 0, with NULL pages, is none), then its own: sequence
+ * b's seq_lens[b] tokens in pages[b][0 .. max_pages). (A prefix whose last
+ * page is not full is followed by a new page.) seq_lens counts the tokens of
+ * the sequence's own pages, the new ones, whose keys are appended before this
+ * call, among them. q: tokens x (n_q_heads * head_dim) of `type` (the cache's:
+ * fp16 or bf16), row stride ldq; n_q_heads is a multiple of n_kv_heads and
+ * query head h reads key head h / (n_q_heads / n_kv_heads). The tokens of
+ * sequence b are rows q_start[b] .. q_start[b + 1] - 1 of q (int32, batch + 1
+ * entries, on the device); NULL is one token per sequence (tokens == batch).
+ * max_q is at least the largest count of them (1 with NULL q_start; rows past
+ * it are left out). New token i of n sees the prefix and its sequence's keys
+ * 0 .. seq_lens[b] - n + i. out: tokens x n_q_heads x head_dim of `type`; lse
+ * (NULL: not wanted): tokens x n_q_heads fp32, the logarithm of the sum of
+ * exp(scale * q.k). A row that sees no key gets zeros and -infinity.
+ *
+ * Logits, maxima, sums and outputs are fp32; the weights are rounded to `type`
+ * for the second product and the output is rounded once. Lengths and page
+ * numbers are read on the device and bounded there: a length is cut to what
+ * max_pages pages hold, a page number outside the cache reads page 0. Memory
+ * past a sequence's length is never used, whatever it holds; a NaN or infinity
+ * in a key or value that some token of a sequence sees may reach the
+ * sequence's other new tokens of the same call.
+ * max_pages bounds the planned work: pass the batch's largest page count.
+ * workspace: lqmm_attn_prefix_workspace_bytes() bytes (partial results; need
+ * not be zeroed; LQMM_ERR_WORKSPACE when smaller); calls that may overlap
+ * must not share it. The result does not depend on timing.
+ */
+lqmm_status lqmm_attn_prefix(const void *q, int64_t ldq, const void *k_cache, const void *v_cache,
+                             int type, const int32_t *prefix_pages, int64_t prefix_len,
+                             const int32_t *pages, int64_t max_pages, const int32_t *seq_lens,
+                             const int32_t *q_start, int64_t max_q, void *out, float *lse,
+                             float scale, int64_t tokens, int64_t batch, int64_t n_q_heads,
+                             int64_t n_kv_heads, int64_t head_dim, int64_t page_size,
+                             int64_t num_pages, void *workspace, size_t workspace_bytes,
+                             void *stream);
+/* Bytes that call needs for these sizes on the current device (0: none, also
+ * for sizes that the call refuses and when there is no device). */
+size_t lqmm_attn_prefix_workspace_bytes(int64_t prefix_len, int64_t max_pages, int64_t max_q,
+                                        int64_t tokens, int64_t batch, int64_t n_q_heads,
+                                        int64_t n_kv_heads, int64_t head_dim, int64_t page_size);
+
+/*
+ * 8-bit float products with a scale for each block of 128. Codes are e4m3
+ * (finite-only, largest value 448). Weights: W is N x K codes, wscale
+ * ceil(N/128) x ceil(K/128) fp32 (one for each 128 x 128 block, the last ones
+ * cut short by N and K). Activations: Xq is M x K codes, xscale ceil(K/128) x
+ * M fp32: xscale[b * M + m] belongs to columns 128b .. 128b + 127 of row m.
+ *   Y[m][n] = sum_k Xq[m][k] xscale[k/128][m] W[n][k] wscale[n/128][k/128]
+ * with fp32 accumulation, rounded once to y_type (fp32, fp16 or bf16). Y is
+ * M x N. K is a multiple of 16 and < LQMM_GEMM_MAX_K; any M and N.
+ */
+lqmm_status lqmm_gemm_f8b128(const uint8_t *W, const float *wscale, const uint8_t *Xq,
+                             const float *xscale, void *Y, int y_type, int64_t M, int64_t N,
+                             int64_t K, void *stream);
+
+/*
+ * Activations to that form: for each row and group of 128 columns
+ *   scale = max(max |x| / 448, 2^-126),  code = x / scale to nearest even.
+ * X: M x K of x_type (fp32, fp16, bf16), row stride ldx; Xq: M x K codes;
+ * xscale: ceil(K/128) x M. K is a multiple of 16. A NaN gives a NaN code; an
+ * infinity makes its whole group's products NaN.
+ */
+lqmm_status lqmm_quant_f8b128(const void *X, int x_type, int64_t ldx, uint8_t *Xq, float *xscale,
+                              int64_t M, int64_t K, void *stream);
 
 /* Workspace the GEMV calls of these sizes can use, in bytes (0 = none):
  * enough for every GEMV entry point on any device. */
