@@ -180,7 +180,8 @@ lqmm_status lqmm_attn_prefix(const void *q, int64_t ldq, const void *k_cache, co
   a.lse = lse;
   a.ldq = ldq;
   a.num_pages = num_pages;
-  a.scale_log2 = scale * 1.4426950408889634f;
+  a.scale_log2 = fmaxf(fabsf(scale) * 1.4426950408889634f, 0x1p-126f);
+  a.q_sign = scale < 0 ? 0x80008000u : 0u;
   return done(lqmm::attn_prefix_launch(a, workspace, e, (hipStream_t)stream));
 }
 

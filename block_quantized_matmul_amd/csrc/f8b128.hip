@@ -234,6 +234,122 @@ gemm_f8b128_kernel(const uint8_t *__restrict__ W, const float *__restrict__ sw,
   }
 }
 
+// Few rows of X (decode): bound by reading W once. A workgroup takes 16 * TN
+// rows of W; its waves share K, wave w taking a contiguous run of scale
+// blocks, and their sums are added in LDS in a fixed order. W and X go
+// straight from memory to the operands, DEPTH blocks ahead, in registers.
+constexpr int kRowWaves = 8;
+
+template <class T, bool F8, int TM, int TN, int DEPTH>
+__global__ void __launch_bounds__(64 * kRowWaves)
+gemm_f8b128_rows_kernel(const uint8_t *__restrict__ W, const float *__restrict__ sw,
+                        const uint8_t *__restrict__ X, const float *__restrict__ sx,
+                        typename T::elem *__restrict__ Y, int M, int64_t N, int64_t K) {
+  constexpr int kN = 16 * TN, kM = 16 * TM, kLd = kN + 4;
+  __shared__ __attribute__((aligned(16))) float part[kRowWaves][kM][kLd];
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int l16 = lane & 15, g = lane >> 4;
+  const int64_t n0 = (int64_t)blockIdx.x * kN;
+  const int m0 = blockIdx.y * kM;
+  const int blocks = (int)((K + BK - 1) / BK);
+  const int per = (blocks + kRowWaves - 1) / kRowWaves;
+  const int kb0 = wave * per, kb1 = kb0 + per < blocks ? kb0 + per : blocks;
+  const uint32_t Ku = (uint32_t)K;
+
+  const int64_t wrows = N - n0 < kN ? N - n0 : kN;
+  const int xrows = M - m0 < kM ? M - m0 : kM;
+  // rows past the ends read zeros
+  const rsrc_t wr = make_rsrc(W + n0 * K, (uint32_t)(wrows * K));
+  const rsrc_t xr = make_rsrc(X + m0 * K, (uint32_t)(xrows * K));
+  const float *swr = sw + (n0 / 128) * blocks;
+
+  struct Stage {
+    u32x4 w[TN][2], x[TM][2];
+    float sx[TM], sw;
+  } st[DEPTH];
+  const uint32_t off = (uint32_t)l16 * Ku + 16 * g;
+  auto load = [&](Stage &s, int kb) {
+    const uint32_t c = (uint32_t)kb * BK;
+#pragma unroll
+    for (int j = 0; j < TN; ++j)
+#pragma unroll
+      for (int u = 0; u < 2; ++u) s.w[j][u] = buf_load_b128(wr, off + 16 * j * Ku + 64 * u + c);
+#pragma unroll
+    for (int i = 0; i < TM; ++i) {
+#pragma unroll
+      for (int u = 0; u < 2; ++u) s.x[i][u] = buf_load_b128(xr, off + 16 * i * Ku + 64 * u + c);
+      const int m = 16 * i + l16;
+      s.sx[i] = sx[(int64_t)kb * M + m0 + (m < xrows ? m : 0)];
+    }
+    s.sw = swr[kb];
+  };
+  auto operand = [&](const u32x4 (&v)[2]) {
+    Operand<F8> o;
+    o.set(__builtin_bit_cast(i32x8, __builtin_shufflevector(v[0], v[1], 0, 1, 2, 3, 4, 5, 6, 7)));
+    return o;
+  };
+
+  float4_t acc[TM][TN];
+#pragma unroll
+  for (int i = 0; i < TM; ++i)
+#pragma unroll
+    for (int j = 0; j < TN; ++j) acc[i][j] = float4_t{0.f, 0.f, 0.f, 0.f};
+
+#pragma unroll
+  for (int d = 0; d < DEPTH; ++d)
+    if (kb0 + d < kb1) load(st[d], kb0 + d);
+  for (int kb = kb0; kb < kb1; kb += DEPTH) {
+#pragma unroll
+    for (int d = 0; d < DEPTH; ++d) {
+      if (kb + d >= kb1) break;
+      Stage &s = st[d];
+      // past K the next row begins
+      if (kb + d == blocks - 1 && Ku % BK != 0) {
+        const u32x4 zero = {0u, 0u, 0u, 0u};
+#pragma unroll
+        for (int u = 0; u < 2; ++u)
+          if ((uint32_t)(kb + d) * BK + 16 * g + 64 * u >= Ku) {
+#pragma unroll
+            for (int j = 0; j < TN; ++j) s.w[j][u] = zero;
+#pragma unroll
+            for (int i = 0; i < TM; ++i) s.x[i][u] = zero;
+          }
+      }
+      Operand<F8> w[TN];
+#pragma unroll
+      for (int j = 0; j < TN; ++j) w[j] = operand(s.w[j]);
+#pragma unroll
+      for (int i = 0; i < TM; ++i) {
+        const Operand<F8> x = operand(s.x[i]);
+        const float f = s.sx[i] * s.sw;
+#pragma unroll
+        for (int j = 0; j < TN; ++j) {
+          const float4_t p = block_sum(w[j], x);
+#pragma unroll
+          for (int r = 0; r < 4; ++r) acc[i][j][r] += p[r] * f;
+        }
+      }
+      if (kb + d + DEPTH < kb1) load(s, kb + d + DEPTH);
+    }
+  }
+
+#pragma unroll
+  for (int i = 0; i < TM; ++i)
+#pragma unroll
+    for (int j = 0; j < TN; ++j)
+      *reinterpret_cast<float4_t *>(&part[wave][16 * i + l16][16 * j + 4 * g]) = acc[i][j];
+  __syncthreads();
+  for (int o = tid; o < kM * kN; o += 64 * kRowWaves) {
+    const int m = o / kN, n = o % kN;
+    if (m >= xrows || n >= wrows) continue;
+    float y = 0.f;
+#pragma unroll
+    for (int w = 0; w < kRowWaves; ++w) y += part[w][m][n];
+    Y[(int64_t)(m0 + m) * N + n0 + n] = (typename T::elem)y;
+  }
+}
+
 template <class T, int BM, int BN, int WM, int WN>
 hipError_t launch_tile(const uint8_t *W, const float *sw, const uint8_t *X, const float *sx, void *Y,
                        int64_t M, int64_t N, int64_t K, hipStream_t stream) {
@@ -248,9 +364,25 @@ hipError_t launch_tile(const uint8_t *W, const float *sw, const uint8_t *X, cons
   return hipGetLastError();
 }
 
+template <class T, int TM, int TN, int DEPTH>
+hipError_t launch_rows(const uint8_t *W, const float *sw, const uint8_t *X, const float *sx, void *Y,
+                       int64_t M, int64_t N, int64_t K, hipStream_t stream) {
+  const int64_t grid = (N + 16 * TN - 1) / (16 * TN);
+  if (grid > 0x7fffffff) return hipErrorInvalidValue;
+  hipLaunchKernelGGL((gemm_f8b128_rows_kernel<T, __is_same(T, TypeBF16), TM, TN, DEPTH>),
+                     dim3((unsigned)grid, (unsigned)((M + 16 * TM - 1) / (16 * TM))),
+                     dim3(64 * kRowWaves), 0, stream, W, sw, X, sx,
+                     static_cast<typename T::elem *>(Y), (int)M, N, K);
+  return hipGetLastError();
+}
+
 template <class T>
 hipError_t launch_gemm(const uint8_t *W, const float *sw, const uint8_t *X, const float *sx, void *Y,
                        int64_t M, int64_t N, int64_t K, hipStream_t stream) {
+  if (M <= 16) return launch_rows<T, 1, 1, 4>(W, sw, X, sx, Y, M, N, K, stream);
+  if (M <= 32) return launch_rows<T, 2, 1, 4>(W, sw, X, sx, Y, M, N, K, stream);
+  if (M <= 48) return launch_rows<T, 3, 1, 2>(W, sw, X, sx, Y, M, N, K, stream);
+  if (M <= 64) return launch_rows<T, 4, 1, 2>(W, sw, X, sx, Y, M, N, K, stream);
   return launch_tile<T, 128, 128, 2, 2>(W, sw, X, sx, Y, M, N, K, stream);
 }
 

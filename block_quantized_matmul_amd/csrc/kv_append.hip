@@ -113,13 +113,13 @@ kv_append_kernel(KvAppend a) {
     return;
   }
 
-  // V of tokens t0 .. t0 + 7. A token whose slot starts a group, followed by
+  // V of tokens t0 .. t0 + 7 and some of the heads. A token whose slot starts a group, followed by
   // seven tokens with the next seven slots, leads a whole group, which is
   // stored as vectors (it may reach into the next workgroup's tokens); a
   // token inside such a group is skipped; any other is stored by itself.
   __shared__ int64_t slot[24];
   __shared__ int lead[16];
-  const int64_t t0 = (int64_t)(blockIdx.x - a.rot_blocks) * 8;
+  const int64_t t0 = (int64_t)((blockIdx.x - a.rot_blocks) / a.v_blocks) * 8;
   if (tid < 22) {
     const int64_t t = t0 - 7 + tid;
     int64_t s = -1;
@@ -137,36 +137,48 @@ kv_append_kernel(KvAppend a) {
     lead[tid] = l;
   }
   __syncthreads();
-  const int half = D / 2, pairs_all = a.n_kv_heads * half;  // two elements per thread
-  const in_t *v = static_cast<const in_t *>(a.v);
-  cache_t *vc = static_cast<cache_t *>(a.v_cache);
+  // Two elements of one head per thread; the eight tokens' loads go out
+  // together (a workgroup of scattered tokens waits for memory once).
+  const int half = D / 2;
+  const int h = (int)((blockIdx.x - a.rot_blocks) % a.v_blocks) * (kThreads / half) + tid / half;
+  const int d = 2 * (tid % half);
+  if (tid / half >= kThreads / half || h >= a.n_kv_heads) return;
+  const in_t *src = static_cast<const in_t *>(a.v) + t0 * a.ldv + (int64_t)h * D + d;
+  cache_t *vc = static_cast<cache_t *>(a.v_cache) + h * head_elems + 8 * d;
+  auto group_of = [&](int64_t s) {
+    return vc + (s >> a.page_log2) * a.n_kv_heads * head_elems +
+           ((s & ((1 << a.page_log2) - 1)) >> 3) * 8 * D;
+  };
+  float x[8], y[8];
+  bool single[8];
+#pragma unroll
   for (int i = 0; i < 8; ++i) {
     const int64_t s = slot[7 + i];
-    if (s < 0) continue;
     const int before = (int)(s & 7);
-    if (before && before <= 7 + i && lead[7 + i - before]) continue;
-    const int64_t t = t0 + i;
-    const int64_t base = (s >> a.page_log2) * a.n_kv_heads * head_elems +
-                         ((s & ((1 << a.page_log2) - 1)) >> 3) * 8 * D;
-    const bool whole = lead[7 + i];
-    for (int w = tid; w < pairs_all; w += kThreads) {
-      const int h = w / half, d = 2 * (w % half);
-      const in_t *src = v + t * a.ldv + (int64_t)h * D + d;
-      cache_t *dst = vc + base + h * head_elems + 8 * d;
-      if (whole) {
-        float x[8], y[8];
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          x[j] = (float)src[j * a.ldv];
-          y[j] = (float)src[j * a.ldv + 1];
-        }
-        store8<TC>(dst, x);
-        store8<TC>(dst + 8, y);
-      } else {
-        dst[before] = (cache_t)(float)src[0];
-        dst[8 + before] = (cache_t)(float)src[1];
-      }
+    single[i] = s >= 0 && !lead[7 + i - before];
+    if (single[i]) {
+      x[i] = (float)src[i * a.ldv];
+      y[i] = (float)src[i * a.ldv + 1];
     }
+  }
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    if (single[i]) {
+      cache_t *dst = group_of(slot[7 + i]) + (slot[7 + i] & 7);
+      dst[0] = (cache_t)x[i];
+      dst[8] = (cache_t)y[i];
+    }
+  }
+  for (int i = 0; i < 8; ++i) {
+    if (!lead[7 + i]) continue;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      x[j] = (float)src[(i + j) * a.ldv];
+      y[j] = (float)src[(i + j) * a.ldv + 1];
+    }
+    cache_t *dst = group_of(slot[7 + i]);
+    store8<TC>(dst, x);
+    store8<TC>(dst + 8, y);
   }
 }
 
@@ -189,7 +201,9 @@ hipError_t kv_append_launch(KvAppend a, ElemType in, ElemType cache, hipStream_t
   const int items = a.head_dim / 16, nh = a.n_q_heads + a.n_kv_heads;
   a.heads_per_block = kThreads / items;
   a.head_blocks = (nh + a.heads_per_block - 1) / a.heads_per_block;
-  const int64_t rot = a.tokens * a.head_blocks, vb = (a.tokens + 7) / 8;
+  const int v_heads = kThreads / (a.head_dim / 2);
+  a.v_blocks = (a.n_kv_heads + v_heads - 1) / v_heads;
+  const int64_t rot = a.tokens * a.head_blocks, vb = (a.tokens + 7) / 8 * a.v_blocks;
   if (rot + vb > 0x7fffffff) return hipErrorInvalidValue;
   a.rot_blocks = (int)rot;
   const int64_t blocks = rot + vb;

@@ -162,7 +162,7 @@ struct KvAppend {
   int64_t ldq, ldk, ldv, tokens, num_pages;
   int n_q_heads, n_kv_heads, head_dim, rot_dim, interleaved, page_log2;
   // set by the launch
-  int heads_per_block, head_blocks, rot_blocks;
+  int heads_per_block, head_blocks, rot_blocks, v_blocks;
 };
 hipError_t kv_append_launch(KvAppend a, ElemType in, ElemType cache, hipStream_t stream);
 
@@ -175,10 +175,12 @@ struct AttnPrefix {
   float *lse;
   int64_t ldq, tokens, batch, max_q, num_pages, max_pages, prefix_len;
   int n_q_heads, n_kv_heads, head_dim, page_log2;
-  float scale_log2;  // scale * log2(e)
+  float scale_log2;  // |scale| * log2(e), > 0 (a scale of 0 is the least that keeps -inf * scale)
+  uint32_t q_sign;   // 0x80008000 for a negative scale: q is negated instead
   // plan (attn_prefix_plan)
   int group, prefix_row_blocks, prefix_chunk, prefix_parts;
   int suffix_row_blocks, suffix_chunk, suffix_parts;
+  int prefix_wide, suffix_wide;  // waves of the wide kernel's workgroups (0: 16-row kernel)
   int64_t prefix_items, suffix_items;
   float *part_o;    // parts x (tokens x heads) x head_dim
   float2 *part_ml;  // parts x (tokens x heads): reference, sum

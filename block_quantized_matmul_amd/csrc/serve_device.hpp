@@ -90,4 +90,18 @@ __device__ __forceinline__ float sum_over_rows(float v) {
   return __builtin_bit_cast(float, b0) + __builtin_bit_cast(float, b1);
 }
 
+// The same over the two half-waves.
+__device__ __forceinline__ float max_over_halves(float v) {
+  const uint32_t u = __builtin_bit_cast(uint32_t, v);
+  const auto a = __builtin_amdgcn_permlane32_swap(u, u, false, false);
+  const uint32_t a0 = a[0], a1 = a[1];
+  return fmaxf(__builtin_bit_cast(float, a0), __builtin_bit_cast(float, a1));
+}
+__device__ __forceinline__ float sum_over_halves(float v) {
+  const uint32_t u = __builtin_bit_cast(uint32_t, v);
+  const auto a = __builtin_amdgcn_permlane32_swap(u, u, false, false);
+  const uint32_t a0 = a[0], a1 = a[1];
+  return __builtin_bit_cast(float, a0) + __builtin_bit_cast(float, a1);
+}
+
 }  // namespace lqmm
