@@ -19,6 +19,7 @@ The shared library is loaded on first use; if it has not been built
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 
 __all__ = [
@@ -151,7 +152,7 @@ def _dev_tensor(t, dtype, name):
     torch = _torch()
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
-    if t.device.type != "cuda":
+    if not t.is_cuda:
         raise ValueError(f"{name} must be a device tensor")
     if t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
@@ -388,45 +389,88 @@ def lqmm_gemv_i4g32(Wq, scales, zeros, x, N, out=None, workspace=None, stream=No
 
 # ---- serving operators ---------------------------------------------------------
 
+# A call's host time is part of a decode step (these calls take a few
+# microseconds on the GPU), so the bindings below look torch up once, read the
+# device and the stream as plain integers, and switch devices only when the
+# tensors are not on the current one.
+class _Torch:
+    torch = None
+
+
+def _serve():
+    """torch and the library, set up on first use."""
+    if _Torch.torch is None:
+        torch = _torch()
+        _Torch.lib = load()
+        _Torch.f32, _Torch.f8, _Torch.u8 = torch.float32, torch.float8_e4m3fn, torch.uint8
+        _Torch.i32, _Torch.i64 = torch.int32, torch.int64
+        _Torch.codes = {torch.float32: 0, torch.float16: 1, torch.bfloat16: 2}
+        _Torch.get_device, _Torch.raw_stream = torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream
+        _Torch.torch = torch
+    return _Torch
+
+
+def _index_of(*ts):
+    """The device that all tensors are on, as an index."""
+    d = ts[0].get_device()
+    for t in ts:
+        if t.get_device() != d:
+            raise ValueError("all tensors must be on the same device")
+    return d
+
+
+def _call(index, stream, fn, *args):
+    """fn(*args, stream) on device ``index``."""
+    T = _Torch
+    if stream is None:
+        stream = T.raw_stream(index)
+    elif not isinstance(stream, int):
+        stream = stream.cuda_stream
+    if T.get_device() == index:
+        status = fn(*args, stream)
+    else:
+        with T.torch.cuda.device(index):
+            status = fn(*args, stream)
+    if status:
+        _check(status)
+
+
 def _type_code(dtype, name, allowed):
     """lqmm_type value of a torch dtype."""
-    torch = _torch()
-    code = {torch.float32: 0, torch.float16: 1, torch.bfloat16: 2}.get(dtype)
-    if code is None or code not in allowed:
+    code = _Torch.codes.get(dtype)
+    if code not in allowed:
         raise TypeError(f"{name} has element type {dtype}, which this call does not take")
     return code
 
 
 def _rows(t, heads, dim, name):
     """(tokens, heads, dim) with contiguous rows: its row stride in elements."""
-    torch = _torch()
-    if not isinstance(t, torch.Tensor):
+    if not isinstance(t, _Torch.torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
-    if t.device.type != "cuda":
+    if not t.is_cuda:
         raise ValueError(f"{name} must be a device tensor")
-    if t.dim() != 3 or t.shape[1] != heads or t.shape[2] != dim:
-        raise ValueError(f"{name} must be (tokens, {heads}, {dim}), got {tuple(t.shape)}")
-    s = t.stride()
+    shape, s = t.shape, t.stride()
+    if len(shape) != 3 or shape[1] != heads or shape[2] != dim:
+        raise ValueError(f"{name} must be (tokens, {heads}, {dim}), got {tuple(shape)}")
     if s[2] != 1 or (heads > 1 and s[1] != dim):
         raise ValueError(f"the heads of one token of {name} must be contiguous")
-    return s[0] if t.shape[0] > 1 else heads * dim
+    return s[0] if shape[0] > 1 else heads * dim
 
 
 def _cache(k_cache, v_cache):
     """Checks the two caches; (num_pages, n_kv_heads, page_size, head_dim, type)."""
-    torch = _torch()
-    for t, name in ((k_cache, "k_cache"), (v_cache, "v_cache")):
-        if not isinstance(t, torch.Tensor):
-            raise TypeError(f"{name} must be a torch.Tensor")
-        _dev_tensor(t, t.dtype, name)
-    if k_cache.dim() != 4:
+    if not isinstance(k_cache, _Torch.torch.Tensor):
+        raise TypeError("k_cache must be a torch.Tensor")
+    dtype = k_cache.dtype
+    _dev_tensor(k_cache, dtype, "k_cache")
+    _dev_tensor(v_cache, dtype, "v_cache")
+    shape = k_cache.shape
+    if len(shape) != 4:
         raise ValueError("k_cache must be (num_pages, n_kv_heads, page_size, head_dim)")
-    pages, hkv, ps, d = k_cache.shape
-    if ps % 8 or tuple(v_cache.shape) != (pages, hkv, ps // 8, d, 8):
+    pages, hkv, ps, d = shape
+    if ps % 8 or v_cache.shape != (pages, hkv, ps // 8, d, 8):
         raise ValueError("v_cache must be (num_pages, n_kv_heads, page_size / 8, head_dim, 8)")
-    if v_cache.dtype != k_cache.dtype:
-        raise TypeError("k_cache and v_cache differ in element type")
-    return pages, hkv, ps, d, _type_code(k_cache.dtype, "k_cache", (1, 2))
+    return pages, hkv, ps, d, _type_code(dtype, "k_cache", (1, 2))
 
 
 def kv_cache_empty(num_pages, n_kv_heads, page_size, head_dim, dtype=None, device="cuda"):
@@ -460,48 +504,45 @@ def lqmm_kv_append(q, k, v, positions, slots, k_cache, v_cache, rope_turns=None,
     Returns the rotated q in the caches' type (q may be None: returns None).
     positions: int32; rope_turns: the table of lqmm_rope_turns, None rotates
     nothing."""
-    torch = _torch()
+    T = _serve()
     pages, hkv, ps, d, ctype = _cache(k_cache, v_cache)
     ldk, ldv = _rows(k, hkv, d, "k"), _rows(v, hkv, d, "v")
-    tokens = k.shape[0]
-    itype = _type_code(k.dtype, "k", (0, 1, 2))
-    if v.dtype != k.dtype or v.shape[0] != tokens:
+    tokens, dtype = k.shape[0], k.dtype
+    itype = _type_code(dtype, "k", (0, 1, 2))
+    if v.dtype != dtype or v.shape[0] != tokens:
         raise ValueError("k and v must have the same element type and tokens")
-    _dev_tensor(slots, torch.int64, "slots")
-    devs = [k, v, slots, k_cache, v_cache]
+    _dev_tensor(slots, T.i64, "slots")
+    if slots.numel() != tokens:
+        raise ValueError(f"slots must have {tokens} entries")
+    index = _index_of(k, v, slots, k_cache, v_cache)
     rot, pos_ptr, turns_ptr = 0, None, None
     if rope_turns is not None:
-        _dev_tensor(rope_turns, torch.int64, "rope_turns")
-        _dev_tensor(positions, torch.int32, "positions")
+        _dev_tensor(rope_turns, T.i64, "rope_turns")
+        _dev_tensor(positions, T.i32, "positions")
         if positions.numel() != tokens:
             raise ValueError(f"positions must have {tokens} entries")
         rot, pos_ptr, turns_ptr = 2 * rope_turns.numel(), positions.data_ptr(), rope_turns.data_ptr()
-        devs += [rope_turns, positions]
-    if slots.numel() != tokens:
-        raise ValueError(f"slots must have {tokens} entries")
+        _index_of(k, rope_turns, positions)
     hq, ldq, q_ptr, out_ptr = 0, 0, None, None
     if q is not None:
-        if not isinstance(q, torch.Tensor) or q.dim() != 3:
+        if not isinstance(q, T.torch.Tensor) or q.dim() != 3:
             raise ValueError("q must be (tokens, n_q_heads, head_dim)")
         hq = q.shape[1]
         ldq = _rows(q, hq, d, "q")
-        if q.dtype != k.dtype or q.shape[0] != tokens:
+        if q.dtype != dtype or q.shape[0] != tokens:
             raise ValueError("q and k must have the same element type and tokens")
         if q_out is None:
-            q_out = torch.empty((tokens, hq, d), dtype=k_cache.dtype, device=k_cache.device)
+            q_out = T.torch.empty((tokens, hq, d), dtype=k_cache.dtype, device=k_cache.device)
         _dev_tensor(q_out, k_cache.dtype, "q_out")
-        if tuple(q_out.shape) != (tokens, hq, d):
+        if q_out.shape != (tokens, hq, d):
             raise ValueError("q_out has the wrong shape")
         q_ptr, out_ptr = q.data_ptr(), q_out.data_ptr()
-        devs += [q, q_out]
+        _index_of(k, q, q_out)
     elif q_out is not None:
         raise ValueError("q_out without q")
-    dev = _same_device(*devs)
-    with torch.cuda.device(dev):
-        _check(load().lqmm_kv_append(q_ptr, k.data_ptr(), v.data_ptr(), itype, ldq, ldk, ldv,
-                                     pos_ptr, slots.data_ptr(), turns_ptr, rot, int(interleaved),
-                                     out_ptr, k_cache.data_ptr(), v_cache.data_ptr(), ctype, tokens,
-                                     hq, hkv, d, ps, pages, _stream(stream)))
+    _call(index, stream, T.lib.lqmm_kv_append, q_ptr, k.data_ptr(), v.data_ptr(), itype, ldq, ldk,
+          ldv, pos_ptr, slots.data_ptr(), turns_ptr, rot, 1 if interleaved else 0, out_ptr,
+          k_cache.data_ptr(), v_cache.data_ptr(), ctype, tokens, hq, hkv, d, ps, pages)
     return q_out
 
 
@@ -519,12 +560,12 @@ def lqmm_attn_prefix_workspace_bytes(prefix_len, max_pages, max_q, tokens, batch
 _scratch = {}
 
 
-def _scratch_for(device, stream_handle, nbytes):
-    torch = _torch()
-    bufs = _scratch.setdefault((device.index, int(stream_handle or 0)), [])
+def _scratch_for(index, stream_handle, nbytes):
+    torch = _Torch.torch
+    bufs = _scratch.setdefault((index, stream_handle), [])
     if not bufs or bufs[-1].numel() < nbytes:
         grown = max(nbytes, 2 * bufs[-1].numel() if bufs else 1 << 20)
-        bufs.append(torch.empty(grown, dtype=torch.uint8, device=device))
+        bufs.append(torch.empty(grown, dtype=torch.uint8, device=torch.device("cuda", index)))
     return bufs[-1]
 
 
@@ -539,74 +580,85 @@ def lqmm_attn_prefix(q, k_cache, v_cache, pages, seq_lens, prefix_pages=None, pr
     most ``max_q`` of them. scale: 1 / sqrt(head_dim) when None. Returns out
     (tokens, n_q_heads, head_dim), or (out, lse) with lse (tokens, n_q_heads)
     float32 when return_lse is set or lse is given."""
-    torch = _torch()
+    T = _serve()
     npages, hkv, ps, d, ctype = _cache(k_cache, v_cache)
-    if not isinstance(q, torch.Tensor) or q.dim() != 3:
+    if not isinstance(q, T.torch.Tensor) or q.dim() != 3:
         raise ValueError("q must be (tokens, n_q_heads, head_dim)")
-    tokens, hq = q.shape[0], q.shape[1]
+    tokens, hq, _ = q.shape
     ldq = _rows(q, hq, d, "q")
-    if q.dtype != k_cache.dtype:
+    dtype = q.dtype
+    if dtype != k_cache.dtype:
         raise TypeError("q must have the caches' element type")
-    _dev_tensor(pages, torch.int32, "pages")
-    _dev_tensor(seq_lens, torch.int32, "seq_lens")
+    _dev_tensor(pages, T.i32, "pages")
+    _dev_tensor(seq_lens, T.i32, "seq_lens")
     if pages.dim() != 2 or seq_lens.dim() != 1 or pages.shape[0] != seq_lens.shape[0]:
         raise ValueError("pages must be (batch, max_pages) and seq_lens (batch,)")
     batch, max_pages = pages.shape
-    devs = [q, k_cache, v_cache, pages, seq_lens]
-    start_ptr = prefix_ptr = lse_ptr = None
+    index = _index_of(q, k_cache, v_cache, pages, seq_lens)
+    start_ptr = prefix_ptr = lse_ptr = ws_ptr = None
     if q_start is not None:
-        _dev_tensor(q_start, torch.int32, "q_start")
+        _dev_tensor(q_start, T.i32, "q_start")
         if q_start.numel() != batch + 1:
             raise ValueError(f"q_start must have {batch + 1} entries")
+        _index_of(q, q_start)
         start_ptr = q_start.data_ptr()
-        devs.append(q_start)
-    prefix_len = int(prefix_len)
+    prefix_len, max_q, ws_bytes = int(prefix_len), int(max_q), 0
     if prefix_len:
-        _dev_tensor(prefix_pages, torch.int32, "prefix_pages")
+        _dev_tensor(prefix_pages, T.i32, "prefix_pages")
         if prefix_pages.numel() * ps < prefix_len:
             raise ValueError("prefix_pages hold fewer than prefix_len tokens")
+        _index_of(q, prefix_pages)
         prefix_ptr = prefix_pages.data_ptr()
-        devs.append(prefix_pages)
     if out is None:
-        out = torch.empty((tokens, hq, d), dtype=q.dtype, device=q.device)
-    _dev_tensor(out, q.dtype, "out")
-    if tuple(out.shape) != (tokens, hq, d):
-        raise ValueError("out has the wrong shape")
-    devs.append(out)
-    if return_lse and lse is None:
-        lse = torch.empty((tokens, hq), dtype=torch.float32, device=q.device)
+        out = T.torch.empty((tokens, hq, d), dtype=dtype, device=q.device)
+    else:
+        _dev_tensor(out, dtype, "out")
+        if out.shape != (tokens, hq, d):
+            raise ValueError("out has the wrong shape")
+        _index_of(q, out)
     if lse is not None:
-        _dev_tensor(lse, torch.float32, "lse")
+        _dev_tensor(lse, T.f32, "lse")
         if lse.numel() != tokens * hq:
             raise ValueError("lse has the wrong size")
+        _index_of(q, lse)
+    elif return_lse:
+        lse = T.torch.empty((tokens, hq), dtype=T.f32, device=q.device)
+    if lse is not None:
         lse_ptr = lse.data_ptr()
-        devs.append(lse)
     if scale is None:
         scale = d ** -0.5
-    lib = load()
-    dev = _same_device(*devs)
-    with torch.cuda.device(dev):
-        st = _stream(stream)
-        need = lib.lqmm_attn_prefix_workspace_bytes(prefix_len, max_pages, max_q, tokens, batch, hq,
-                                                    hkv, d, ps)
-        ws_ptr, ws_bytes = None, 0
-        if workspace is None and need:
-            workspace = _scratch_for(dev, st, need)
-        if workspace is not None:
-            _dev_tensor(workspace, torch.uint8, "workspace")
+    if stream is None:
+        stream = T.raw_stream(index)
+    elif not isinstance(stream, int):
+        stream = stream.cuda_stream
+    if workspace is None:
+        need = _attn_need(index, prefix_len, max_pages, max_q, tokens, batch, hq, hkv, d, ps)
+        if need:
+            workspace = _scratch_for(index, stream, need)
             ws_ptr, ws_bytes = workspace.data_ptr(), workspace.numel()
-        _check(lib.lqmm_attn_prefix(q.data_ptr(), ldq, k_cache.data_ptr(), v_cache.data_ptr(), ctype,
-                                    prefix_ptr, prefix_len, pages.data_ptr(), max_pages,
-                                    seq_lens.data_ptr(), start_ptr, max_q, out.data_ptr(), lse_ptr,
-                                    scale, tokens, batch, hq, hkv, d, ps, npages, ws_ptr, ws_bytes,
-                                    st))
+    else:
+        _dev_tensor(workspace, T.u8, "workspace")
+        _index_of(q, workspace)
+        ws_ptr, ws_bytes = workspace.data_ptr(), workspace.numel()
+    _call(index, stream, T.lib.lqmm_attn_prefix, q.data_ptr(), ldq, k_cache.data_ptr(),
+          v_cache.data_ptr(), ctype, prefix_ptr, prefix_len, pages.data_ptr(), max_pages,
+          seq_lens.data_ptr(), start_ptr, max_q, out.data_ptr(), lse_ptr, scale, tokens, batch, hq,
+          hkv, d, ps, npages, ws_ptr, ws_bytes)
     return (out, lse) if lse is not None else out
+
+
+@functools.lru_cache(maxsize=4096)
+def _attn_need(index, *sizes):
+    """lqmm_attn_prefix_workspace_bytes on device ``index`` (a function of the
+    sizes alone, asked for every decode step)."""
+    with _Torch.torch.cuda.device(index):
+        return _Torch.lib.lqmm_attn_prefix_workspace_bytes(*sizes)
 
 
 def _codes(t, name):
     """A 2-D contiguous tensor of e4m3 codes (float8_e4m3fn or raw uint8)."""
-    torch = _torch()
-    if not isinstance(t, torch.Tensor) or t.dtype not in (torch.float8_e4m3fn, torch.uint8):
+    T = _Torch
+    if not isinstance(t, T.torch.Tensor) or t.dtype not in (T.f8, T.u8):
         raise TypeError(f"{name} must be a float8_e4m3fn (or uint8) torch.Tensor")
     _dev_tensor(t, t.dtype, name)
     if t.dim() != 2:
@@ -618,28 +670,34 @@ def lqmm_quant_f8b128(X, out=None, scales=None, stream=None):
     """X (M, K) float32, float16 or bfloat16 (rows may be strided) to e4m3 codes
     with a scale per row and 128 columns: (codes (M, K) float8_e4m3fn, scales
     (ceil(K / 128), M) float32)."""
-    torch = _torch()
-    if not isinstance(X, torch.Tensor) or X.dim() != 2:
+    T = _serve()
+    if not isinstance(X, T.torch.Tensor) or X.dim() != 2:
         raise ValueError("X must be (M, K)")
-    if X.device.type != "cuda":
+    if not X.is_cuda:
         raise ValueError("X must be a device tensor")
     M, K = X.shape
-    if K > 1 and X.stride(1) != 1:
+    ld, s1 = X.stride()
+    if K > 1 and s1 != 1:
         raise ValueError("the rows of X must be contiguous")
     xtype = _type_code(X.dtype, "X", (0, 1, 2))
     blocks = (K + 127) // 128
+    index = X.get_device()
     if out is None:
-        out = torch.empty((M, K), dtype=torch.float8_e4m3fn, device=X.device)
+        out = T.torch.empty((M, K), dtype=T.f8, device=X.device)
+    else:
+        _codes(out, "out")
+        if out.shape != (M, K):
+            raise ValueError("out has the wrong shape")
+        _index_of(X, out)
     if scales is None:
-        scales = torch.empty((blocks, M), dtype=torch.float32, device=X.device)
-    _codes(out, "out")
-    _dev_tensor(scales, torch.float32, "scales")
-    if tuple(out.shape) != (M, K) or tuple(scales.shape) != (blocks, M):
-        raise ValueError("out or scales has the wrong shape")
-    dev = _same_device(X, out, scales)
-    with torch.cuda.device(dev):
-        _check(load().lqmm_quant_f8b128(X.data_ptr(), xtype, X.stride(0) if M > 1 else K,
-                                        out.data_ptr(), scales.data_ptr(), M, K, _stream(stream)))
+        scales = T.torch.empty((blocks, M), dtype=T.f32, device=X.device)
+    else:
+        _dev_tensor(scales, T.f32, "scales")
+        if scales.shape != (blocks, M):
+            raise ValueError("scales has the wrong shape")
+        _index_of(X, scales)
+    _call(index, stream, T.lib.lqmm_quant_f8b128, X.data_ptr(), xtype, ld if M > 1 else K,
+          out.data_ptr(), scales.data_ptr(), M, K)
     return out, scales
 
 
@@ -648,26 +706,25 @@ def lqmm_gemm_f8b128(W, wscale, Xq, xscale, out=None, out_dtype=None, stream=Non
     with wscale (ceil(N / 128), ceil(K / 128)), Xq (M, K) with xscale
     (ceil(K / 128), M) as lqmm_quant_f8b128 makes them. out_dtype: float16
     (default), bfloat16 or float32."""
-    torch = _torch()
+    T = _serve()
     _codes(W, "W")
     _codes(Xq, "Xq")
-    _dev_tensor(wscale, torch.float32, "wscale")
-    _dev_tensor(xscale, torch.float32, "xscale")
-    (N, K), M = W.shape, Xq.shape[0]
-    if Xq.shape[1] != K:
+    _dev_tensor(wscale, T.f32, "wscale")
+    _dev_tensor(xscale, T.f32, "xscale")
+    (N, K), (M, K2) = W.shape, Xq.shape
+    if K2 != K:
         raise ValueError(f"shape mismatch: W {tuple(W.shape)} Xq {tuple(Xq.shape)}")
     blocks = (K + 127) // 128
-    if tuple(wscale.shape) != ((N + 127) // 128, blocks) or tuple(xscale.shape) != (blocks, M):
+    if wscale.shape != ((N + 127) // 128, blocks) or xscale.shape != (blocks, M):
         raise ValueError("wscale or xscale has the wrong shape")
     if out is None:
-        out = torch.empty((M, N), dtype=out_dtype or torch.float16, device=W.device)
+        out = T.torch.empty((M, N), dtype=out_dtype or T.torch.float16, device=W.device)
+    else:
+        _dev_tensor(out, out_dtype or out.dtype, "out")
+        if out.shape != (M, N):
+            raise ValueError("out has the wrong shape")
     ytype = _type_code(out.dtype, "out", (0, 1, 2))
-    _dev_tensor(out, out_dtype or out.dtype, "out")
-    if tuple(out.shape) != (M, N):
-        raise ValueError("out has the wrong shape")
-    dev = _same_device(W, wscale, Xq, xscale, out)
-    with torch.cuda.device(dev):
-        _check(load().lqmm_gemm_f8b128(W.data_ptr(), wscale.data_ptr(), Xq.data_ptr(),
-                                       xscale.data_ptr(), out.data_ptr(), ytype, M, N, K,
-                                       _stream(stream)))
+    index = _index_of(W, wscale, Xq, xscale, out)
+    _call(index, stream, T.lib.lqmm_gemm_f8b128, W.data_ptr(), wscale.data_ptr(), Xq.data_ptr(),
+          xscale.data_ptr(), out.data_ptr(), ytype, M, N, K)
     return out
