@@ -344,18 +344,6 @@ struct Wide {
   static constexpr int kLds = kStages * 2 * kHalf + kMaxIds * 4;
 };
 
-template <int N>
-__device__ __forceinline__ void wait_loads_and_barrier() {
-  asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(N) : "memory");
-}
-
-typedef __attribute__((address_space(1))) const void *global_ptr;
-typedef __attribute__((address_space(3))) void *lds_ptr;
-__device__ __forceinline__ void load_to_lds(const void *src, uint8_t *dst) {
-  __builtin_amdgcn_global_load_lds((global_ptr)(uintptr_t)src,
-                                   (lds_ptr)dst, 16, 0, 0);
-}
-
 template <class T, int D, int NW>
 __global__ void __launch_bounds__(64 * NW, D <= 128 ? 2 : 1)
 attn_wide_kernel(AttnPrefix a, uint32_t item0) {
@@ -429,9 +417,9 @@ attn_wide_kernel(AttnPrefix a, uint32_t item0) {
       const int u = (wave * kLoads + i) * 64 + lane;  // 16-byte unit of the tile
       const int r = u / kChunks, c = (u % kChunks) ^ (r & kSwz);
       const int key = (r & ~15) + 8 * (r >> 2 & 1) + 4 * (r >> 3 & 1) + (r & 3);
-      load_to_lds(kc + group_at(j0 + (key & ~7)) + (key & 7) * D + 8 * c,
+      load_to_lds<16>(kc + group_at(j0 + (key & ~7)) + (key & 7) * D + 8 * c,
                   ks + (wave * kLoads + i) * 1024);
-      load_to_lds(vc + group_at(j0 + 8 * (u / D)) + (u % D) * 8, vs + (wave * kLoads + i) * 1024);
+      load_to_lds<16>(vc + group_at(j0 + 8 * (u / D)) + (u % D) * 8, vs + (wave * kLoads + i) * 1024);
     }
   };
 

@@ -129,27 +129,49 @@ __device__ __forceinline__ float4_t block_sum(const Operand<false> &a, const Ope
   return p;
 }
 
-// BM x BN tile (rows of X by rows of W), WM x WN waves.
-template <class T, int BM, int BN, int WM, int WN>
-__global__ void __launch_bounds__(64 * WM * WN)
+// A BM x BN tile (rows of X by rows of W). WK groups of WM x WN waves share
+// it: a step of the K loop is WK scale blocks, each group takes one of them,
+// and the groups' sums are added in LDS at the end, in a fixed order. NS LDS
+// stages.
+template <int BM, int BN, int WM, int WN, int WK, int NS>
+struct Tile {
+  static constexpr int kWaves = WM * WN * WK;
+  static constexpr int kCodes = (BM + BN) * BK;         // bytes of a block's codes
+  static constexpr int kPart = kCodes + (BM + 64) * 4;  // with the scales of its rows, and of W
+  static constexpr int kStage = WK * kPart;
+  static constexpr int kGroup = WM * WN;                // waves that load and use a block
+  static constexpr int kLoads = (BM + BN) / 8 / kGroup; // 1 KB loads of a wave per step
+  static constexpr int kSums = (WK - 1) * BM * BN * 4;  // bytes of the groups' sums
+  static constexpr int kLds = NS * kStage > kSums ? NS * kStage : kSums;
+};
+
+template <class T, int BM, int BN, int WM, int WN, int WK, int NS>
+__global__ void __launch_bounds__(64 * WM * WN * WK)
 gemm_f8b128_kernel(const uint8_t *__restrict__ W, const float *__restrict__ sw,
                    const uint8_t *__restrict__ X, const float *__restrict__ sx,
-                   typename T::elem *__restrict__ Y, int64_t M, int64_t N, int64_t K, int tiles_m) {
+                   typename T::elem *__restrict__ Y, int64_t M, int64_t N, int64_t K, int tiles_m,
+                   int tiles_n) {
+  typedef Tile<BM, BN, WM, WN, WK, NS> C;
   constexpr bool F8 = __is_same(T, TypeBF16);
-  constexpr int kWaves = WM * WN;
   constexpr int TM = BM / WM / 16, TN = BN / WN / 16;  // 16 x 16 tiles of a wave
-  constexpr int kStage = (BM + BN) * BK;
-  constexpr int kLoads = (BM + BN) / 8 / kWaves;  // 1 KB loads of a wave per step
-  static_assert((BM + BN) / 8 % kWaves == 0 && BN / WN <= 128 && 128 % (BN / WN) == 0, "tile");
+  constexpr int kScaleLoads = (BM + 63) / 64;          // waves of a group that bring scales of X
+  static_assert((BM + BN) / 8 % C::kGroup == 0 && BN / WN <= 128 && 128 % (BN / WN) == 0, "tile");
+  static_assert(BM % 64 == 0 && kScaleLoads <= C::kGroup, "scale loads");
   extern __shared__ __attribute__((aligned(16))) uint8_t smem[];
 
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int wk = wave / C::kGroup, gw = wave % C::kGroup;  // block of the step, wave of the group
   const int l16 = lane & 15, g = lane >> 4;
-  const int tile = blockIdx.x;
-  const int64_t m0 = (int64_t)(tile % tiles_m) * BM, n0 = (int64_t)(tile / tiles_m) * BN;
-  const int wm = (wave % WM) * (BM / WM), wn = (wave / WM) * (BN / WN);
-  const int blocks = (int)((K + BK - 1) / BK);
+  // Workgroups go to the 8 XCDs in turn; consecutive tiles (the M tiles of one
+  // W tile) are put on one XCD, whose L2 then holds the W tile once.
+  const uint32_t tiles = (uint32_t)tiles_m * tiles_n;
+  const uint32_t xcd = blockIdx.x % 8, q8 = tiles / 8, r8 = tiles % 8;
+  const uint32_t tile = xcd * q8 + (xcd < r8 ? xcd : r8) + blockIdx.x / 8;
+  const int64_t m0 = (int64_t)(tile % (uint32_t)tiles_m) * BM;
+  const int64_t n0 = (int64_t)(tile / (uint32_t)tiles_m) * BN;
+  const int wm = (gw % WM) * (BM / WM), wn = (gw / WM) * (BN / WN);
+  const int blocks = (int)((K + BK - 1) / BK), steps = (blocks + WK - 1) / WK;
   const uint32_t Ku = (uint32_t)K;
 
   const int64_t xrows = M - m0 < BM ? M - m0 : BM;
@@ -161,14 +183,24 @@ gemm_f8b128_kernel(const uint8_t *__restrict__ W, const float *__restrict__ sw,
   // c ^ (r & 7), so that the eight rows that one phase of a 16-byte LDS read
   // touches lie in different banks. A load fills 8 rows, lane by lane.
   const int lrow = lane >> 3, lcol = 16 * ((lane & 7) ^ lrow);
-  auto issue = [&](int kt) {
-    uint8_t *st = smem + (kt & 1) * kStage;
+  // The block's scales: wave w < BM / 64 of the group brings those of rows
+  // 64 w .. of X; the last wave those of the tile's 128-row blocks of W (the
+  // others in between the same again; with too few waves, an extra load).
+  constexpr bool kExtra = kScaleLoads == C::kGroup;  // the last wave brings both
+  const bool x_scales = gw < kScaleLoads;
+  const int64_t sm = m0 + 64 * gw + lane;
+  const float *sxp = sx + (sm < M ? sm : M - 1);
+  const int64_t nb = n0 / 128 + lane % (BN > 128 ? BN / 128 : 1), last_nb = (N - 1) / 128;
+  const float *swp = sw + (nb < last_nb ? nb : last_nb) * blocks;
+  auto issue = [&](int step) {
+    uint8_t *st = smem + (step % NS) * C::kStage + wk * C::kPart;
+    const int kt = step * WK + wk;
     // past K the rows of the next line begin: those chunks read as zeros
     // (an offset past the resource)
     const bool in = (uint32_t)(kt * BK + lcol) < Ku;
 #pragma unroll
-    for (int i = 0; i < kLoads; ++i) {
-      const int j = wave * kLoads + i;  // 8 rows: X first, then W
+    for (int i = 0; i < C::kLoads; ++i) {
+      const int j = gw * C::kLoads + i;  // 8 rows: X first, then W
       const bool is_x = j < BM / 8;
       const int r = 8 * (is_x ? j : j - BM / 8) + lrow;
       const int off = in ? (int)((uint32_t)r * Ku + lcol) : (int)0x80000000u;
@@ -177,7 +209,13 @@ gemm_f8b128_kernel(const uint8_t *__restrict__ W, const float *__restrict__ sw,
       else
         __builtin_amdgcn_raw_ptr_buffer_load_lds(wr, st + j * 1024, 16, off, kt * BK, 0, 0);
     }
+    const int b = kt < blocks ? kt : blocks - 1;
+    const bool xs_here = x_scales;
+    load_to_lds<4>(xs_here ? sxp + (int64_t)b * M : swp + b,
+                   st + C::kCodes + (xs_here ? gw * 256 : BM * 4));
+    if constexpr (kExtra) load_to_lds<4>(swp + b, st + C::kCodes + BM * 4);
   };
+  constexpr int kStepLoads = C::kLoads + (kExtra ? 2 : 1);
   auto frag = [&](const uint8_t *base, int row) {
     const int s = row & 7;
     const i32x4 lo = *reinterpret_cast<const i32x4 *>(base + row * BK + 16 * (g ^ s));
@@ -185,40 +223,93 @@ gemm_f8b128_kernel(const uint8_t *__restrict__ W, const float *__restrict__ sw,
     return __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
   };
 
-  const int64_t nblk = (n0 + wn) / 128;
-  const bool n_in = n0 + wn < N;
   float4_t acc[TM][TN];
 #pragma unroll
   for (int i = 0; i < TM; ++i)
 #pragma unroll
     for (int j = 0; j < TN; ++j) acc[i][j] = float4_t{0.f, 0.f, 0.f, 0.f};
-
-  issue(0);
-  for (int kt = 0; kt < blocks; ++kt) {
-    asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
-    if (kt + 1 < blocks) issue(kt + 1);
-    const uint8_t *xst = smem + (kt & 1) * kStage, *wst = xst + BM * BK;
-    const float s_n = n_in ? sw[nblk * blocks + kt] : 0.f;
-    float s[TM];
+  // The block sums of the 16 rows before, and their scale: they are added
+  // while the matrix cores work on the next 16.
+  float4_t p[TN];
+  float s_prev = 0.f;
 #pragma unroll
-    for (int i = 0; i < TM; ++i) {
-      const int64_t m = m0 + wm + 16 * i + l16;
-      s[i] = m < M ? sx[(int64_t)kt * M + m] * s_n : 0.f;
-    }
+  for (int j = 0; j < TN; ++j) p[j] = float4_t{0.f, 0.f, 0.f, 0.f};
+  // Operands of X that are read ahead: all of a step's when they fit in
+  // registers beside the sums, else one.
+  constexpr int kAhead = TM + TN <= 8 ? TM : 2;
+
+#pragma unroll
+  for (int d = 0; d < NS - 1; ++d)
+    if (d < steps) issue(d);
+  for (int kt = 0; kt < steps; ++kt) {
+    // the loads of step kt are done when only those of the later steps are out
+    if (kt + NS - 2 < steps)
+      wait_loads_and_barrier<(NS - 2) * kStepLoads>();
+    else
+      wait_loads_and_barrier<0>();
+    if (kt + NS - 1 < steps) issue(kt + NS - 1);
+    const uint8_t *xst = smem + (kt % NS) * C::kStage + wk * C::kPart, *wst = xst + BM * BK;
+    const float *scales = reinterpret_cast<const float *>(xst + C::kCodes);
+    const float s_n = scales[BM + wn / 128];
+    i32x8 wraw[TN], xraw[kAhead];
+#pragma unroll
+    for (int j = 0; j < TN; ++j) wraw[j] = frag(wst, wn + 16 * j + l16);
+#pragma unroll
+    for (int i = 0; i < (kAhead == TM ? TM : 1); ++i) xraw[i] = frag(xst, wm + 16 * i + l16);
     Operand<F8> wf[TN];
 #pragma unroll
-    for (int j = 0; j < TN; ++j) wf[j].set(frag(wst, wn + 16 * j + l16));
+    for (int j = 0; j < TN; ++j) wf[j].set(wraw[j]);
+    if constexpr (F8) __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
     for (int i = 0; i < TM; ++i) {
+      if (kAhead != TM && i + 1 < TM) xraw[(i + 1) % kAhead] = frag(xst, wm + 16 * (i + 1) + l16);
+      const float s = scales[wm + 16 * i + l16] * s_n;
       Operand<F8> xf;
-      xf.set(frag(xst, wm + 16 * i + l16));
+      xf.set(xraw[i % kAhead]);
 #pragma unroll
       for (int j = 0; j < TN; ++j) {
-        const float4_t p = block_sum(wf[j], xf);
+        const float4_t q = block_sum(wf[j], xf);
 #pragma unroll
-        for (int r = 0; r < 4; ++r) acc[i][j][r] += p[r] * s[i];
+        for (int r = 0; r < 4; ++r) acc[(i + TM - 1) % TM][j][r] += p[j][r] * s_prev;
+        p[j] = q;
+      }
+      s_prev = s;
+      if constexpr (F8) {
+        // matrix and vector instructions in turn
+        __builtin_amdgcn_sched_group_barrier(0x100, 3, 0);  // the next operand and a scale
+#pragma unroll
+        for (int j = 0; j < TN; ++j) {
+          __builtin_amdgcn_sched_group_barrier(0x8, 1, 0);
+          __builtin_amdgcn_sched_group_barrier(0x2, 4, 0);
+        }
+        __builtin_amdgcn_sched_barrier(0);
       }
     }
+  }
+#pragma unroll
+  for (int j = 0; j < TN; ++j)
+#pragma unroll
+    for (int r = 0; r < 4; ++r) acc[TM - 1][j][r] += p[j][r] * s_prev;
+
+  if constexpr (WK > 1) {
+    // sums of group k > 0, each lane's values together: the same lane of group
+    // 0 adds them
+    float4_t *sums = reinterpret_cast<float4_t *>(smem);
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < TM; ++i)
+#pragma unroll
+      for (int j = 0; j < TN; ++j)
+        if (wk > 0) sums[(((wk - 1) * C::kGroup + gw) * TM * TN + i * TN + j) * 64 + lane] = acc[i][j];
+    __syncthreads();
+    if (wk > 0) return;
+#pragma unroll
+    for (int k = 1; k < WK; ++k)
+#pragma unroll
+      for (int i = 0; i < TM; ++i)
+#pragma unroll
+        for (int j = 0; j < TN; ++j)
+          acc[i][j] += sums[(((k - 1) * C::kGroup + gw) * TM * TN + i * TN + j) * 64 + lane];
   }
 
   const bool vec = N % 4 == 0;
@@ -350,17 +441,17 @@ gemm_f8b128_rows_kernel(const uint8_t *__restrict__ W, const float *__restrict__
   }
 }
 
-template <class T, int BM, int BN, int WM, int WN>
+template <class T, int BM, int BN, int WM, int WN, int WK, int NS>
 hipError_t launch_tile(const uint8_t *W, const float *sw, const uint8_t *X, const float *sx, void *Y,
                        int64_t M, int64_t N, int64_t K, hipStream_t stream) {
-  constexpr int kLds = 2 * (BM + BN) * BK;
-  constexpr auto kern = gemm_f8b128_kernel<T, BM, BN, WM, WN>;
+  constexpr int kLds = Tile<BM, BN, WM, WN, WK, NS>::kLds;
+  constexpr auto kern = gemm_f8b128_kernel<T, BM, BN, WM, WN, WK, NS>;
   const int64_t tm = (M + BM - 1) / BM, tn = (N + BN - 1) / BN;
   if (tm * tn > 0x7fffffff) return hipErrorInvalidValue;
   const hipError_t e = ensure_max_lds<kern>(kLds);
   if (e != hipSuccess) return e;
-  hipLaunchKernelGGL(kern, dim3((unsigned)(tm * tn)), dim3(64 * WM * WN), kLds, stream, W, sw, X, sx,
-                     static_cast<typename T::elem *>(Y), M, N, K, (int)tm);
+  hipLaunchKernelGGL(kern, dim3((unsigned)(tm * tn)), dim3(64 * WM * WN * WK), kLds, stream, W, sw, X, sx,
+                     static_cast<typename T::elem *>(Y), M, N, K, (int)tm, (int)tn);
   return hipGetLastError();
 }
 
@@ -378,12 +469,53 @@ hipError_t launch_rows(const uint8_t *W, const float *sw, const uint8_t *X, cons
 
 template <class T>
 hipError_t launch_gemm(const uint8_t *W, const float *sw, const uint8_t *X, const float *sx, void *Y,
-                       int64_t M, int64_t N, int64_t K, hipStream_t stream) {
-  if (M <= 16) return launch_rows<T, 1, 1, 4>(W, sw, X, sx, Y, M, N, K, stream);
-  if (M <= 32) return launch_rows<T, 2, 1, 4>(W, sw, X, sx, Y, M, N, K, stream);
-  if (M <= 48) return launch_rows<T, 3, 1, 2>(W, sw, X, sx, Y, M, N, K, stream);
-  if (M <= 64) return launch_rows<T, 4, 1, 2>(W, sw, X, sx, Y, M, N, K, stream);
-  return launch_tile<T, 128, 128, 2, 2>(W, sw, X, sx, Y, M, N, K, stream);
+                       int64_t M, int64_t N, int64_t K, int num_cus, hipStream_t stream) {
+  // Up to 16 rows: W is read once, by 16 of its rows a workgroup; by 64 when
+  // that still gives most CUs one and X is worth sharing. Measured (K = 4096,
+  // us, 16 / 64 rows of W): M = 16, N = 4096 7.1 / 12.5, N = 14336 17.9 / 13.9,
+  // N = 28672 and K = 8192 63 / 54; M = 1, N = 28672 and K = 8192 42 / 50.
+  if (M <= 16) {
+    if (M > 4 && N >= 48 * (int64_t)num_cus)
+      return launch_rows<T, 1, 4, 2>(W, sw, X, sx, Y, M, N, K, stream);
+    return launch_rows<T, 1, 1, 4>(W, sw, X, sx, Y, M, N, K, stream);
+  }
+  // Up to 32 rows and one workgroup a CU, the same: M = 32, N = 4096 9.2
+  // against 12.1 for the tiles below, N = 7000 14.4 against 10.7.
+  if (M <= 32 && N <= 16 * (int64_t)num_cus)
+    return launch_rows<T, 2, 1, 2>(W, sw, X, sx, Y, M, N, K, stream);
+
+  // Tiles: the one whose rounds over the CUs cost least. Cost of a round per
+  // scale block, measured at K = 4096 (ns; f8 cores / fp16 cores).
+  constexpr bool F8 = __is_same(T, TypeBF16);
+  struct Choice {
+    int bm, bn, per_cu, cost;
+  };
+  constexpr Choice kChoices[] = {
+      {64, 32, 1, F8 ? 270 : 330},   {64, 64, 1, F8 ? 310 : 400},    {64, 64, 2, F8 ? 510 : 800},
+      {128, 128, 1, F8 ? 750 : 1100}, {128, 256, 1, F8 ? 1300 : 2050}, {256, 256, 1, F8 ? 2000 : 9999}};
+  int best = 0;
+  int64_t best_cost = 0;
+  for (int c = 0; c < 6; ++c) {
+    const Choice &o = kChoices[c];
+    const int64_t tiles = ((M + o.bm - 1) / o.bm) * ((N + o.bn - 1) / o.bn);
+    const int64_t slots = (int64_t)o.per_cu * num_cus;
+    const int64_t cost = (tiles + slots - 1) / slots * o.cost;
+    if (c == 0 || cost < best_cost) {
+      best = c;
+      best_cost = cost;
+    }
+  }
+  switch (best) {
+    case 0: return launch_tile<T, 64, 32, 1, 1, 4, 3>(W, sw, X, sx, Y, M, N, K, stream);
+    case 1: return launch_tile<T, 64, 64, 1, 2, 4, 2>(W, sw, X, sx, Y, M, N, K, stream);
+    case 2: return launch_tile<T, 64, 64, 1, 2, 2, 2>(W, sw, X, sx, Y, M, N, K, stream);
+    case 3: return launch_tile<T, 128, 128, 2, 2, 2, 2>(W, sw, X, sx, Y, M, N, K, stream);
+    case 4: return launch_tile<T, 128, 256, 2, 4, 1, 3>(W, sw, X, sx, Y, M, N, K, stream);
+  }
+  // (fp16 cores: never the best, their operands do not fit beside 256 x 256 sums)
+  if constexpr (F8)
+    return launch_tile<T, 256, 256, 2, 4, 1, 2>(W, sw, X, sx, Y, M, N, K, stream);
+  return hipErrorInvalidValue;
 }
 
 template <class T>
@@ -408,10 +540,9 @@ hipError_t quant_f8b128_launch(const void *X, ElemType type, int64_t ldx, uint8_
 hipError_t gemm_f8b128_launch(const uint8_t *W, const float *sw, const uint8_t *X, const float *sx,
                               void *Y, ElemType type, int64_t M, int64_t N, int64_t K, int num_cus,
                               hipStream_t stream) {
-  (void)num_cus;
-  if (type == ElemType::F32) return launch_gemm<TypeF32>(W, sw, X, sx, Y, M, N, K, stream);
-  if (type == ElemType::F16) return launch_gemm<TypeF16>(W, sw, X, sx, Y, M, N, K, stream);
-  return launch_gemm<TypeBF16>(W, sw, X, sx, Y, M, N, K, stream);
+  if (type == ElemType::F32) return launch_gemm<TypeF32>(W, sw, X, sx, Y, M, N, K, num_cus, stream);
+  if (type == ElemType::F16) return launch_gemm<TypeF16>(W, sw, X, sx, Y, M, N, K, num_cus, stream);
+  return launch_gemm<TypeBF16>(W, sw, X, sx, Y, M, N, K, num_cus, stream);
 }
 
 }  // namespace lqmm

@@ -104,4 +104,24 @@ __device__ __forceinline__ float sum_over_halves(float v) {
   return __builtin_bit_cast(float, a0) + __builtin_bit_cast(float, a1);
 }
 
+// Waits until at most N of this wave's memory loads are out and its LDS
+// operations are done, then joins the workgroup barrier.
+template <int N>
+__device__ __forceinline__ void wait_loads_and_barrier() {
+  asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(N) : "memory");
+}
+
+// BYTES (4 or 16) of each lane from src to LDS: lane i's go to dst + BYTES * i
+// (dst is the same in all lanes).
+typedef __attribute__((address_space(1))) const void *global_ptr;
+typedef __attribute__((address_space(3))) void *lds_ptr;
+template <int BYTES>
+__device__ __forceinline__ void load_to_lds(const void *src, uint8_t *dst) {
+  static_assert(BYTES == 4 || BYTES == 16, "load size");
+  if constexpr (BYTES == 16)
+    __builtin_amdgcn_global_load_lds((global_ptr)(uintptr_t)src, (lds_ptr)dst, 16, 0, 0);
+  else
+    __builtin_amdgcn_global_load_lds((global_ptr)(uintptr_t)src, (lds_ptr)dst, 4, 0, 0);
+}
+
 }  // namespace lqmm

@@ -374,6 +374,33 @@ def test_f8_product(M, N, K, t):
     assert rel <= 1e-5 + u and top <= 1e-4 + u, (rel, top)
 
 
+@pytest.mark.parametrize("M, N, K, t", [
+    (300, 3000, 1040, "bf16"), (300, 3000, 144, "f16"), (700, 8300, 400, "bf16"),
+    (700, 8300, 272, "f32"), (1500, 9000, 384, "bf16"), (1500, 9000, 256, "f16"),
+    (2900, 9100, 400, "bf16"), (2900, 9100, 272, "f16"), (16, 12300, 144, "f16"),
+    (9, 12301, 1040, "bf16"), (32, 4000, 2064, "f32"), (20, 300, 16, "bf16"),
+])
+def test_f8_product_large(M, N, K, t):
+    """Every tile size, ends in all three directions; expected values in 64
+    bits on the GPU."""
+    w, ws, x, xs = make_f8(M, N, K, M + N + K)
+    announce(f"gemm_f8b128 {M}x{N}x{K} {t}")
+    dw, dx = f8_dev(w), f8_dev(x)
+    dws, dxs = torch.from_numpy(ws).to(DEV), torch.from_numpy(xs).to(DEV)
+    got = bq.lqmm_gemm_f8b128(dw, dws, dx, dxs, out_dtype=DT[t]).double()
+    kb = torch.arange(K, device=DEV) // 128
+    W = dw.double() * dws.double()[torch.arange(N, device=DEV) // 128][:, kb]
+    want = torch.matmul(dx.double() * dxs.double()[kb].t(), W.t().contiguous())
+    if t == "f16":
+        big = want.abs() > 65504
+        assert torch.isinf(got[want.abs() > 65536]).all()
+        got, want = got.masked_fill(big, 0), want.masked_fill(big, 0)
+    rel = float((got - want).norm() / want.norm())
+    top = float((got - want).abs().max() / want.abs().max())
+    u = 0.0 if t == "f32" else so.U[t]
+    assert rel <= 1e-5 + u and top <= 1e-4 + u, (rel, top)
+
+
 def test_f8_product_is_exact_on_integers():
     """Products and sums that fp32 holds exactly come out exactly."""
     r = np.random.default_rng(5)
