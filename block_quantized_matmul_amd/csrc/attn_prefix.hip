@@ -122,25 +122,28 @@ __device__ __forceinline__ uint32_t spread(uint32_t block, uint32_t n) {
 }
 
 // ---- few rows -------------------------------------------------------------------
-template <class T, int D>
-__global__ void __launch_bounds__(kThreads)
-attn_rows16_kernel(AttnPrefix a, uint32_t item0) {
+template <int D, int NW>
+struct Rows16 {
+  static constexpr int kPass = D / 16 < 8 ? D / 16 : 8;  // O tiles joined at a time
+  static constexpr int kLd = 16 * kPass + 4;
+  int ids[kMaxIds];
+  float wave_m[NW][kRows], wave_l[NW][kRows];
+  __attribute__((aligned(16))) float join[NW][kRows][kLd];
+};
+
+template <class T, int D, int NW>
+__device__ __forceinline__ void rows16_body(const AttnPrefix &a, const Item &it, Rows16<D, NW> &sm) {
   typedef typename T::elem elem;
   typedef typename T::vec8 vec8;
   constexpr int kQ = D / 32;                       // k-steps of one logit tile
   constexpr int kDT = D / 16;                      // 16-wide tiles of O
-  constexpr int kPass = kDT < 8 ? kDT : 8;         // O tiles joined at a time
-  constexpr int kLd = 16 * kPass + 4;
+  constexpr int kPass = Rows16<D, NW>::kPass;
   static_assert(kDT % kPass == 0, "whole passes");
-  __shared__ int ids[kMaxIds];
-  __shared__ float wave_m[4][kRows], wave_l[4][kRows];
-  __shared__ __attribute__((aligned(16))) float join[4][kRows][kLd];
+  int *ids = sm.ids;
 
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int m16 = lane & 15, g = lane >> 4;
-  Item it;
-  if (!find_item(a, item0 + spread(blockIdx.x, gridDim.x), kRows, it)) return;
   const int G = a.group;
   const int lg = a.page_log2, pmask = (1 << lg) - 1;
   const bool direct = a.prefix_parts + a.suffix_parts == 1;
@@ -149,7 +152,7 @@ attn_rows16_kernel(AttnPrefix a, uint32_t item0) {
   const int page0 = it.c0 >> lg;
   if (it.c1 > it.c0) {
     const int n = ((it.c1 - 1) >> lg) - page0 + 1;
-    for (int i = tid; i < n; i += kThreads) {
+    for (int i = tid; i < n; i += 64 * NW) {
       const int32_t p = it.pages[page0 + i];
       ids[i] = (uint32_t)p < (uint32_t)a.num_pages ? p : 0;
     }
@@ -202,7 +205,7 @@ attn_rows16_kernel(AttnPrefix a, uint32_t item0) {
 
   int j0 = it.c0 + wave * kStep;
   if (j0 < it.c1) load_k(j0);
-  for (; j0 < it.c1; j0 += 4 * kStep) {
+  for (; j0 < it.c1; j0 += NW * kStep) {
     vec8 vf[kDT];
     {
       const int64_t base = group_at(clamp_group(j0 + 8 * g));
@@ -217,7 +220,7 @@ attn_rows16_kernel(AttnPrefix a, uint32_t item0) {
 #pragma unroll
       for (int i = 0; i < kQ; ++i) s[u] = T::mfma16(kf[u][i], q[i], s[u]);
     }
-    if (j0 + 4 * kStep < it.c1) load_k(j0 + 4 * kStep);
+    if (j0 + NW * kStep < it.c1) load_k(j0 + NW * kStep);
     float z[2][4];
 #pragma unroll
     for (int u = 0; u < 2; ++u)
@@ -266,26 +269,27 @@ attn_rows16_kernel(AttnPrefix a, uint32_t item0) {
     }
   }
 
-  // Join the four waves' results.
+  // Join the waves' results.
   l = sum_over_rows(l);
   if (g == 0) {
-    wave_m[wave][m16] = m;
-    wave_l[wave][m16] = l;
+    sm.wave_m[wave][m16] = m;
+    sm.wave_l[wave][m16] = l;
   }
   __syncthreads();
   float mj = -INFINITY;
 #pragma unroll
-  for (int w = 0; w < 4; ++w) mj = fmaxf(mj, wave_m[w][m16]);
+  for (int w = 0; w < NW; ++w) mj = fmaxf(mj, sm.wave_m[w][m16]);
+  constexpr int kPer = 32 / NW;  // values of a row that a thread writes per pass
   const float mine = m == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(m - mj);
-  const int out_row = tid >> 4, out_d = 8 * (tid & 15);
+  const int out_row = tid / (4 * NW), out_d = kPer * (tid % (4 * NW));
   // the row that this thread writes
   float lj = 0.f, mo = -INFINITY;
 #pragma unroll
-  for (int w = 0; w < 4; ++w) mo = fmaxf(mo, wave_m[w][out_row]);
+  for (int w = 0; w < NW; ++w) mo = fmaxf(mo, sm.wave_m[w][out_row]);
 #pragma unroll
-  for (int w = 0; w < 4; ++w) {
-    const float mw = wave_m[w][out_row];
-    lj += mw == -INFINITY ? 0.f : wave_l[w][out_row] * __builtin_amdgcn_exp2f(mw - mo);
+  for (int w = 0; w < NW; ++w) {
+    const float mw = sm.wave_m[w][out_row];
+    lj += mw == -INFINITY ? 0.f : sm.wave_l[w][out_row] * __builtin_amdgcn_exp2f(mw - mo);
   }
   const int orow = it.row0 + out_row;
   const bool owrite = orow < it.rows;
@@ -299,25 +303,30 @@ attn_rows16_kernel(AttnPrefix a, uint32_t item0) {
       float4_t x = o[pass * kPass + i];
 #pragma unroll
       for (int r = 0; r < 4; ++r) x[r] *= mine;
-      *reinterpret_cast<float4_t *>(&join[wave][m16][16 * i + 4 * g]) = x;
+      *reinterpret_cast<float4_t *>(&sm.join[wave][m16][16 * i + 4 * g]) = x;
     }
     __syncthreads();
     if (owrite && out_d < 16 * kPass) {
-      float x[8];
+      float x[kPer];
 #pragma unroll
-      for (int e = 0; e < 8; ++e)
-        x[e] = (join[0][out_row][out_d + e] + join[1][out_row][out_d + e]) +
-               (join[2][out_row][out_d + e] + join[3][out_row][out_d + e]);
+      for (int e = 0; e < kPer; ++e) {
+        x[e] = sm.join[0][out_row][out_d + e];
+#pragma unroll
+        for (int w = 1; w < NW; ++w) x[e] += sm.join[w][out_row][out_d + e];
+      }
       const int64_t d0 = pass * 16 * kPass + out_d;
       if (direct) {
+        typedef elem out_vec __attribute__((ext_vector_type(kPer)));
         const float inv = lj == 0.f ? 0.f : 1.0f / lj;
+        out_vec y;
 #pragma unroll
-        for (int e = 0; e < 8; ++e) x[e] *= inv;
-        store8<T>(static_cast<elem *>(a.out) + flat * D + d0, x);
+        for (int e = 0; e < kPer; ++e) y[e] = (elem)(x[e] * inv);
+        *reinterpret_cast<out_vec *>(static_cast<elem *>(a.out) + flat * D + d0) = y;
       } else {
         float *dst = a.part_o + (it.part * nrows + flat) * D + d0;
-        *reinterpret_cast<float4_t *>(dst) = float4_t{x[0], x[1], x[2], x[3]};
-        *reinterpret_cast<float4_t *>(dst + 4) = float4_t{x[4], x[5], x[6], x[7]};
+#pragma unroll
+        for (int e = 0; e < kPer; e += 4)
+          *reinterpret_cast<float4_t *>(dst + e) = float4_t{x[e], x[e + 1], x[e + 2], x[e + 3]};
       }
     }
   }
@@ -330,217 +339,395 @@ attn_rows16_kernel(AttnPrefix a, uint32_t item0) {
   }
 }
 
+template <class T, int D>
+__global__ void __launch_bounds__(kThreads)
+attn_rows16_kernel(AttnPrefix a, uint32_t item0) {
+  __shared__ Rows16<D, kThreads / 64> sm;
+  Item it;
+  if (find_item(a, item0 + spread(blockIdx.x, gridDim.x), kRows, it))
+    rows16_body<T, D, kThreads / 64>(a, it, sm);
+}
+
 // ---- many rows -----------------------------------------------------------------
 // A running maximum that grows by no more than kSlack (log2) is left where it
 // is: O is rescaled when a row needs it, not at every step.
 constexpr float kSlack = 8.0f;
 constexpr float kWideShift = 6.0f;  // weights are at most 2^(kSlack + kWideShift), in fp16's range
 
+// Waves of a SIMD that the wide kernel's registers leave room for: two of 32
+// rows, one of 64 rows (two at 64 dimensions) or of 256 dimensions.
+constexpr int wide_waves(int d, int nw, int r) {
+  return r > 1 ? (d == 64 ? 2 : 1) : d <= 128 && nw == 8 ? 2 : 1;
+}
+
 template <int D>
 struct Wide {
   static constexpr int kKeys = D <= 128 ? 64 : 32;  // keys of a tile
   static constexpr int kHalf = kKeys * D * 2;       // bytes of a tile's K (and V)
-  static constexpr int kStages = 3;
-  static constexpr int kLds = kStages * 2 * kHalf + kMaxIds * 4;
+  // a round is two tiles between barriers: K of it and of the tile after, V of
+  // it, and the next round's two tiles of each on their way
+  static constexpr int kStagesK = 5, kStagesV = 4;
+  static constexpr int kLds = (kStagesK + kStagesV) * kHalf;
 };
 
-template <class T, int D, int NW>
-__global__ void __launch_bounds__(64 * NW, D <= 128 ? 2 : 1)
-attn_wide_kernel(AttnPrefix a, uint32_t item0) {
+template <class T, int D, int NW, int R>
+__device__ __forceinline__ void wide_body(const AttnPrefix &a, const Item &it, uint8_t *smem) {
   typedef typename T::elem elem;
   typedef typename T::vec8 vec8;
   typedef Wide<D> C;
   constexpr int KT = C::kKeys;
-  constexpr int kQ = D / 16;                 // k-steps of a logit tile
-  constexpr int kDT = D / 32;                // 32-wide tiles of O
-  constexpr int kSub = KT / 32;
+  constexpr int kQ = D / 16;                    // k-steps of a logit tile
+  constexpr int kDT = D / 32;                   // 32-wide tiles of O
   constexpr int kLoads = C::kHalf / 1024 / NW;  // 1 KB loads of a wave for K, and for V
-  static_assert(C::kHalf % (1024 * NW) == 0, "whole loads");
-  extern __shared__ __attribute__((aligned(16))) uint8_t smem[];
-  int *ids = reinterpret_cast<int *>(smem + C::kStages * 2 * C::kHalf);
-
+  constexpr int kGroups = KT / 8 / NW;          // eight-key groups that a wave loads
+  static_assert(C::kHalf % (1024 * NW) == 0 && KT % (8 * NW) == 0, "whole loads");
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int l32 = lane & 31, h = lane >> 5;
-  Item it;
-  if (!find_item(a, item0 + spread(blockIdx.x, gridDim.x), 32 * NW, it)) return;
   const int G = a.group;
   const int lg = a.page_log2, pmask = (1 << lg) - 1;
   const bool direct = a.prefix_parts + a.suffix_parts == 1;
 
-  const int page0 = it.c0 >> lg;
-  if (it.c1 > it.c0) {
-    const int n = ((it.c1 - 1) >> lg) - page0 + 1;
-    for (int i = tid; i < n; i += 64 * NW) {
-      const int32_t p = it.pages[page0 + i];
-      ids[i] = (uint32_t)p < (uint32_t)a.num_pages ? p : 0;
-    }
-  }
-  const int row0 = it.row0 + 32 * wave;  // this wave's rows
-  const int row = row0 + l32;
-  const bool live = row < it.rows;
-  const int tok = live ? row / G : 0;
-  const int64_t t = it.tok0 + tok;
-  const int hq = it.h * G + (live ? row % G : 0);
-  const int limit = it.past + it.per_token * tok;
-  const int all_see = it.past + it.per_token * (row0 < it.rows ? row0 / G : 0);
-  vec8 q[kQ];
-  {
-    const elem *src = static_cast<const elem *>(a.q) + t * a.ldq + (int64_t)hq * D + 8 * h;
+  // This wave's rows, in R tiles of 32.
+  const int row0 = it.row0 + 32 * R * wave;
+  bool live[R];
+  int64_t flat[R];  // (token, head) of this lane's rows
+  int limit[R];     // keys below it are seen
+  vec8 q[R][kQ];
+#pragma unroll
+  for (int w = 0; w < R; ++w) {
+    const int row = row0 + 32 * w + l32;
+    live[w] = row < it.rows;
+    const int tok = live[w] ? row / G : 0;
+    const int hq = it.h * G + (live[w] ? row % G : 0);
+    flat[w] = (it.tok0 + tok) * a.n_q_heads + hq;
+    limit[w] = it.past + it.per_token * tok;
+    const elem *src = static_cast<const elem *>(a.q) + (it.tok0 + tok) * a.ldq + (int64_t)hq * D + 8 * h;
 #pragma unroll
     for (int i = 0; i < kQ; ++i) {
       const u32x4 x = *reinterpret_cast<const u32x4 *>(src + 16 * i);
-      q[i] = __builtin_bit_cast(vec8, x ^ a.q_sign);
+      q[w][i] = __builtin_bit_cast(vec8, x ^ a.q_sign);
     }
   }
-  __syncthreads();
+  const int all_see = it.past + it.per_token * (row0 < it.rows ? row0 / G : 0);
 
-  // Tile rows of K in LDS are in the order of the logit tile's rows (row m of
-  // 32: key 16 (m / 16) + 8 (m / 4 % 2) + 4 (m / 8 % 2) + m % 4), with their
-  // 16-byte chunks exchanged per row, so that the eight rows of one read
-  // phase lie in different banks. V is as in memory.
-  const elem *kc = static_cast<const elem *>(a.k_cache);
-  const elem *vc = static_cast<const elem *>(a.v_cache);
-  const int64_t head_elems = (int64_t)D << lg;
-  const int last_group = (it.c1 - 1) & ~7;
-  auto group_at = [&](int j) -> int64_t {
-    j = j < last_group ? j : last_group;
-    const int64_t page = ids[(j >> lg) - page0];
-    return (page * a.n_kv_heads + it.h) * head_elems + (int64_t)(j & pmask) * D;
+  // Loads. The eight keys of a group are 16 D bytes in one piece, of K and of
+  // V, at the same offset. A wave brings kGroups groups of a tile: its page
+  // numbers are the same in all lanes (scalar loads and addresses), its lanes'
+  // places in a group are fixed. In LDS, row `key` of K has its 16-byte
+  // chunks exchanged by `swz(key)`, so that the eight rows of one read phase
+  // (keys 0-3 and 8-11, or 4-7 and 12-15) lie in different banks; V is as in
+  // memory.
+  const uint8_t *kc = static_cast<const uint8_t *>(a.k_cache);
+  const uint8_t *vc = static_cast<const uint8_t *>(a.v_cache);
+  const int64_t head_bytes = (int64_t)(2 * D) << lg;
+  constexpr int kChunks = D / 8;  // 16-byte chunks of a row of K
+  auto swz = [](int key) {
+    return D == 96 ? (key & 3) : (key & 3) + 4 * (key >> 3 & 1);
   };
-  constexpr int kChunks = D / 8;  // 16-byte chunks of a row
-  constexpr int kSwz = D == 96 ? 3 : 7;
-  auto issue = [&](int j0, int stage) {
-    uint8_t *ks = smem + stage * 2 * C::kHalf, *vs = ks + C::kHalf;
+  uint32_t koff[kLoads], voff[kLoads];
+#pragma unroll
+  for (int i = 0; i < kLoads; ++i) {
+    const int u = i * 64 + lane;  // 16-byte unit of the wave's groups
+    const int key = 8 * kGroups * wave + u / kChunks;
+    koff[i] = (uint32_t)((u % D / kChunks) * 2 * D + 16 * ((u % kChunks) ^ swz(key)));
+    voff[i] = (uint32_t)(u % D) * 16;
+  }
+  const int last_group = (it.c1 - 1) & ~7;
+  // The page numbers of the wave's groups of a tile, one tile before they are
+  // needed (constant memory: scalar loads, which no pending LDS load holds up).
+  typedef const __attribute__((address_space(4))) int32_t *constant_ptr;
+  const constant_ptr pages = (constant_ptr)(uintptr_t)it.pages;
+  struct Pages {
+    int32_t n[kGroups];
+  };
+  auto key_of_group = [&](int j0, int i) {
+    const int j = j0 + 8 * (kGroups * wave + i);
+    return j < last_group ? j : last_group;
+  };
+  auto pages_of = [&](int j0) {
+    Pages p;
+#pragma unroll
+    for (int i = 0; i < kGroups; ++i) p.n[i] = pages[key_of_group(j0, i) >> lg];
+    return p;
+  };
+  auto load_half = [&](const uint8_t *cache, const uint32_t (&off)[kLoads], int j0, const Pages &p,
+                       uint8_t *dst) {
+    const uint8_t *base[kGroups];
+#pragma unroll
+    for (int i = 0; i < kGroups; ++i) {
+      const int64_t page = (uint32_t)p.n[i] < (uint32_t)a.num_pages ? p.n[i] : 0;
+      const uint64_t at = reinterpret_cast<uint64_t>(cache) +
+                          (uint64_t)((page * a.n_kv_heads + it.h) * head_bytes +
+                                     (int64_t)(key_of_group(j0, i) & pmask) * (2 * D));
+      base[i] = reinterpret_cast<const uint8_t *>(at);
+    }
 #pragma unroll
     for (int i = 0; i < kLoads; ++i) {
-      const int u = (wave * kLoads + i) * 64 + lane;  // 16-byte unit of the tile
-      const int r = u / kChunks, c = (u % kChunks) ^ (r & kSwz);
-      const int key = (r & ~15) + 8 * (r >> 2 & 1) + 4 * (r >> 3 & 1) + (r & 3);
-      load_to_lds<16>(kc + group_at(j0 + (key & ~7)) + (key & 7) * D + 8 * c,
-                  ks + (wave * kLoads + i) * 1024);
-      load_to_lds<16>(vc + group_at(j0 + 8 * (u / D)) + (u % D) * 8, vs + (wave * kLoads + i) * 1024);
+      constexpr int last = kGroups - 1;
+      const int g0 = 64 * i / D, g1 = (64 * i + 63) / D;  // groups that the load touches
+      uint8_t *to = dst + (wave * kLoads + i) * 1024;
+      if (g0 == g1) {  // scalar base, 32-bit lane offsets
+        const rsrc_t r = make_rsrc(base[g0 < last ? g0 : last], 16 * D);
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(r, to, 16, (int)off[i], 0, 0, 0);
+      } else {
+        load_to_lds<16>(((i * 64 + lane) / D == g0 ? base[g0] : base[g1 < last ? g1 : last]) + off[i], to);
+      }
     }
   };
+  // K is used up to one tile before V: the loads go out as pairs K of tile
+  // p + 1, V of tile p.
+  uint8_t *const vsmem = smem + C::kStagesK * C::kHalf;
+  auto k_stage = [&](int tile) { return smem + tile % C::kStagesK * C::kHalf; };
+  auto v_stage = [&](int tile) { return vsmem + tile % C::kStagesV * C::kHalf; };
+  Pages pk, pv;  // of the next pair
+  auto next_pages = [&](int p) {
+    pv = pages_of(it.c0 + p * KT);
+    pk = pages_of(it.c0 + (p + 1) * KT);
+  };
+  auto load_pair = [&](int p) {
+    load_half(kc, koff, it.c0 + (p + 1) * KT, pk, k_stage(p + 1));
+    load_half(vc, voff, it.c0 + p * KT, pv, v_stage(p));
+    next_pages(p + 1);
+  };
 
-  float16_t o[kDT];
+  float16_t o[R][kDT];
+  float m[R], l[R], top[R];
+  float ref[R];  // m - kWideShift, finite
 #pragma unroll
-  for (int i = 0; i < kDT; ++i)
+  for (int w = 0; w < R; ++w) {
+    m[w] = top[w] = -INFINITY;
+    l[w] = ref[w] = 0.f;
 #pragma unroll
-    for (int r = 0; r < 16; ++r) o[i][r] = 0.f;
-  float m = -INFINITY, l = 0.f;
-  float ref = 0.f;  // m - kWideShift, finite
+    for (int i = 0; i < kDT; ++i)
+#pragma unroll
+      for (int r = 0; r < 16; ++r) o[w][i][r] = 0.f;
+  }
 
-  const int tiles = (it.c1 - it.c0 + KT - 1) / KT;
-  if (tiles > 0) issue(it.c0, 0);
-  if (tiles > 1) issue(it.c0 + KT, 1);
-  for (int kt = 0; kt < tiles; ++kt) {
-    const int j0 = it.c0 + kt * KT;
-    if (kt + 1 < tiles)
-      wait_loads_and_barrier<2 * kLoads>();
-    else
-      wait_loads_and_barrier<0>();
-    if (kt + 2 < tiles) issue(j0 + 2 * KT, (kt + 2) % 3);
-    uint8_t *ks = smem + (kt % 3) * 2 * C::kHalf, *vs = ks + C::kHalf;
-    if (j0 + KT > it.c1) {
-      // what lies behind the last key may be anything, and 0 * NaN is NaN
-      const int valid = it.c1 - j0;
-      elem *ve = reinterpret_cast<elem *>(vs);
-      for (int u = tid; u < (KT - valid) * D; u += 64 * NW) {
-        const int key = valid + u / D, d = u % D;
-        ve[((key >> 3) * D + d) * 8 + (key & 7)] = (elem)0.f;
+  // A step is 32 keys. S^T of a step: row m is key 16 (m / 16) + 8 (m / 4 % 2)
+  // + 4 (m / 8 % 2) + m % 4, which leaves the weights of the step's 16-key
+  // halves as the B operands of O^T = V^T P^T.
+  const int key_of_lane = (l32 & 16) + 8 * (l32 >> 2 & 1) + 4 * (l32 >> 3 & 1) + (l32 & 3);
+  constexpr int kM = kQ / 2;  // logit products of half a step
+  static_assert(kM == kDT, "as many products of V in half a step");
+  auto k_operand = [&](const uint8_t *ks, int sub, int i) {
+    const int key = 32 * sub + key_of_lane;
+    return *reinterpret_cast<const vec8 *>(ks + key * (2 * D) + 16 * ((2 * i + h) ^ swz(key)));
+  };
+  auto v_operand = [&](const uint8_t *vs, int half, int i) {  // 16 keys `half`, dimensions 32 i ..
+    return *reinterpret_cast<const vec8 *>(vs + ((2 * half + h) * D + 32 * i + l32) * 16);
+  };
+  typedef float16_t Logits[R];
+  auto mask = [&](int j0, Logits &s) {
+    asm volatile("");  // stays behind its branch: few steps need it
+#pragma unroll
+    for (int w = 0; w < R; ++w) {
+      const int seen = (limit[w] < it.c1 ? limit[w] : it.c1) - j0 - 8 * h;
+#pragma unroll
+      for (int r = 0; r < 16; ++r)
+        if (16 * (r >> 3) + (r & 7) >= seen) s[w][r] = -INFINITY;
+    }
+  };
+  const int plain_end = it.c1 < all_see ? it.c1 : all_see;  // steps up to here need no mask
+
+  // One step: the weights of s (32 keys, V at vs + `sub`) on the vector ALU
+  // beside the logits of the next 32 keys (from jn, K at kn + `nsub`; past the
+  // last key: of what is there, masked) on the matrix cores, then the products
+  // with V beside the next maximum. Each half reads the next one's operands
+  // from LDS, the last one those of K for the step after (K at ka + `asub`;
+  // one-step tiles read them at the step's start, behind the barrier).
+  constexpr bool kCarry = KT == 64;
+  vec8 k0[kM];
+  auto step = [&](const uint8_t *vs, int sub, const Logits &s, const uint8_t *kn, int nsub, int jn,
+                  Logits &next, const uint8_t *ka, int asub) {
+    bool grown = false;
+#pragma unroll
+    for (int w = 0; w < R; ++w) grown = grown || top[w] > m[w] + kSlack;
+    if (__any(grown)) {
+#pragma unroll
+      for (int w = 0; w < R; ++w) {
+        const float mn = fmaxf(m[w], top[w]);
+        const float c = m[w] == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(m[w] - mn);
+        m[w] = mn;
+        ref[w] = (mn == -INFINITY ? 0.f : mn) - kWideShift;
+        l[w] *= c;
+#pragma unroll
+        for (int i = 0; i < kDT; ++i)
+#pragma unroll
+          for (int r = 0; r < 16; ++r) o[w][i][r] *= c;
       }
-      __syncthreads();
     }
-
-    float16_t s[kSub];
+    vec8 p[R][2], k1[kM], vf[2][kDT];
+    if constexpr (!kCarry) {
 #pragma unroll
-    for (int u = 0; u < kSub; ++u) {
+      for (int i = 0; i < kM; ++i) k0[i] = k_operand(kn, nsub, i);
+    }
+    __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-      for (int r = 0; r < 16; ++r) s[u][r] = 0.f;
-      const int r = 32 * u + l32;
+    for (int c = 0; c < 2; ++c) {
+      if (c == 0) {
 #pragma unroll
-      for (int i = 0; i < kQ; ++i) {
-        const vec8 kf = *reinterpret_cast<const vec8 *>(ks + r * (2 * D) + 16 * ((2 * i + h) ^ (r & kSwz)));
-        s[u] = T::mfma32(kf, q[i], s[u]);
+        for (int i = 0; i < kM; ++i) k1[i] = k_operand(kn, nsub, kM + i);
+      } else {
+#pragma unroll
+        for (int i = 0; i < kDT; ++i) vf[0][i] = v_operand(vs, 2 * sub, i);
       }
+#pragma unroll
+      for (int i = 0; i < kM; ++i)
+#pragma unroll
+        for (int w = 0; w < R; ++w)
+          next[w] = T::mfma32(c == 0 ? k0[i] : k1[i], q[w][c * kM + i], c + i == 0 ? float16_t{} : next[w]);
+#pragma unroll
+      for (int w = 0; w < R; ++w) {
+        float sum = 0.f;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const float x = __builtin_amdgcn_exp2f(fmaf(s[w][8 * c + e], a.scale_log2, -ref[w]));
+          sum += x;
+          p[w][c][e] = (elem)x;
+        }
+        l[w] += sum;
+        asm volatile("" : "+v"(p[w][c]));  // computed here, not after the mask's branch
+      }
+      // matrix and vector instructions in turn
+      __builtin_amdgcn_sched_group_barrier(0x100, kM, 0);
+#pragma unroll
+      for (int i = 0; i < R * kM; ++i) {
+        __builtin_amdgcn_sched_group_barrier(0x8, 1, 0);
+        __builtin_amdgcn_sched_group_barrier(0x402, 28 / kM, 0);
+      }
+      __builtin_amdgcn_sched_barrier(0);
     }
-    if (j0 + KT > it.c1 || j0 + KT > all_see) {
-      const int seen = limit < it.c1 ? limit : it.c1;
+    if (jn + 32 > plain_end) mask(jn, next);
+    float x[R];
 #pragma unroll
-      for (int u = 0; u < kSub; ++u)
+    for (int w = 0; w < R; ++w) x[w] = -INFINITY;
 #pragma unroll
-        for (int r = 0; r < 16; ++r)
-          if (j0 + 32 * u + 16 * (r >> 3) + 8 * h + (r & 7) >= seen) s[u][r] = -INFINITY;
-    }
-    float top = s[0][0];
+    for (int c = 0; c < 2; ++c) {
+      if (c == 0) {
 #pragma unroll
-    for (int u = 0; u < kSub; ++u)
+        for (int i = 0; i < kDT; ++i) vf[1][i] = v_operand(vs, 2 * sub + 1, i);
+      } else if constexpr (kCarry) {
 #pragma unroll
-      for (int r = 0; r < 16; ++r) top = fmaxf(top, s[u][r]);
-    top = max_over_halves(top) * a.scale_log2;
-    if (__any(top > m + kSlack)) {
-      const float mn = fmaxf(m, top);
-      const float c = m == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(m - mn);
-      m = mn;
-      ref = (mn == -INFINITY ? 0.f : mn) - kWideShift;
-      l *= c;
+        for (int i = 0; i < kM; ++i) k0[i] = k_operand(ka, asub, i);
+      }
 #pragma unroll
       for (int i = 0; i < kDT; ++i)
 #pragma unroll
-        for (int r = 0; r < 16; ++r) o[i][r] *= c;
+        for (int w = 0; w < R; ++w) o[w][i] = T::mfma32(vf[c][i], p[w][c], o[w][i]);
+#pragma unroll
+      for (int w = 0; w < R; ++w)
+#pragma unroll
+        for (int e = 0; e < 8; e += 2)
+          x[w] = fmaxf(fmaxf(next[w][8 * c + e], next[w][8 * c + e + 1]), x[w]);
+      __builtin_amdgcn_sched_group_barrier(0x100, kDT, 0);
+#pragma unroll
+      for (int i = 0; i < R * kDT; ++i) {
+        __builtin_amdgcn_sched_group_barrier(0x8, 1, 0);
+        __builtin_amdgcn_sched_group_barrier(0x2, 2, 0);
+      }
+      __builtin_amdgcn_sched_barrier(0);
     }
 #pragma unroll
-    for (int u = 0; u < kSub; ++u)
+    for (int w = 0; w < R; ++w) top[w] = max_over_halves(x[w]) * a.scale_log2;
+  };
+
+  const int tiles = (it.c1 - it.c0 + KT - 1) / KT;
+  Logits s, s2;
+  if (tiles > 0) {
+    next_pages(0);
+    load_half(kc, koff, it.c0, pv, smem);
+    load_pair(0);
+    if (tiles > 1) load_pair(1);
+    wait_loads_and_barrier<0>();
 #pragma unroll
-      for (int w = 0; w < 2; ++w) {
-        vec8 p;
+    for (int i = 0; i < kQ; ++i) {
+      const vec8 k = k_operand(smem, 0, i);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          const float x = __builtin_amdgcn_exp2f(fmaf(s[u][8 * w + e], a.scale_log2, -ref));
-          l += x;
-          p[e] = (elem)x;
-        }
+      for (int w = 0; w < R; ++w) s[w] = T::mfma32(k, q[w][i], i == 0 ? float16_t{} : s[w]);
+    }
+    if (it.c0 + 32 > plain_end) mask(it.c0, s);
 #pragma unroll
-        for (int i = 0; i < kDT; ++i) {
-          const vec8 vf = *reinterpret_cast<const vec8 *>(
-              vs + ((4 * u + 2 * w + h) * D + 32 * i + l32) * 16);
-          o[i] = T::mfma32(vf, p, o[i]);
-        }
+    for (int w = 0; w < R; ++w) {
+      float x = s[w][0];
+#pragma unroll
+      for (int r = 1; r < 16; ++r) x = fmaxf(x, s[w][r]);
+      top[w] = max_over_halves(x) * a.scale_log2;
+    }
+    if constexpr (kCarry) {
+#pragma unroll
+      for (int i = 0; i < kM; ++i) k0[i] = k_operand(smem, 1, i);
+    }
+  }
+  for (int round = 0; round < tiles; round += 2) {
+    if (round) wait_loads_and_barrier<0>();
+    if (round + 2 < tiles) load_pair(round + 2);
+    if (round + 3 < tiles) load_pair(round + 3);
+    if (it.c0 + (round + 2) * KT > it.c1) {
+      // What lies behind the last key may be anything, and 0 * NaN is NaN: V
+      // of the round's keys from c1 on is cleared.
+      const int first = it.c1 - it.c0;
+      const int last = (round + 2 < tiles ? round + 2 : tiles) * KT;
+      for (int u = tid; u < (last - first) * D; u += 64 * NW) {
+        const int key = first + u / D, d = u % D, in = key % KT;
+        reinterpret_cast<elem *>(v_stage(key / KT))[((in >> 3) * D + d) * 8 + (in & 7)] = (elem)0.f;
       }
+      __syncthreads();
+    }
+#pragma unroll
+    for (int b = 0; b < 2; ++b) {
+      const int kt = round + b, j0 = it.c0 + kt * KT;
+      if (kt >= tiles) break;
+      const uint8_t *vs = v_stage(kt), *kn = k_stage(kt + 1);
+      if constexpr (KT == 64) {
+        step(vs, 0, s, k_stage(kt), 1, j0 + 32, s2, kn, 0);
+        step(vs, 1, s2, kn, 0, j0 + 64, s, kn, 1);
+      } else {
+        step(vs, 0, s, kn, 0, j0 + 32, s2, nullptr, 0);
+#pragma unroll
+        for (int w = 0; w < R; ++w) s[w] = s2[w];
+      }
+    }
   }
 
-  l = sum_over_halves(l);
-  if (!live) return;
-  const int64_t flat = t * a.n_q_heads + hq;
   const int64_t nrows = a.tokens * a.n_q_heads;
-  if (direct) {
-    typedef elem vec4 __attribute__((ext_vector_type(4)));
-    const float inv = l == 0.f ? 0.f : 1.0f / l;
-    elem *dst = static_cast<elem *>(a.out) + flat * D + 4 * h;
 #pragma unroll
-    for (int i = 0; i < kDT; ++i)
-#pragma unroll
-      for (int r = 0; r < 16; r += 4)
-        *reinterpret_cast<vec4 *>(dst + 32 * i + 2 * r) =
-            vec4{(elem)(o[i][r] * inv), (elem)(o[i][r + 1] * inv), (elem)(o[i][r + 2] * inv),
-                 (elem)(o[i][r + 3] * inv)};
-  } else {
-    float *dst = a.part_o + (it.part * nrows + flat) * D + 4 * h;
-#pragma unroll
-    for (int i = 0; i < kDT; ++i)
-#pragma unroll
-      for (int r = 0; r < 16; r += 4)
-        *reinterpret_cast<float4_t *>(dst + 32 * i + 2 * r) =
-            float4_t{o[i][r], o[i][r + 1], o[i][r + 2], o[i][r + 3]};
-  }
-  if (h == 0) {
+  for (int w = 0; w < R; ++w) {
+    const float sum = sum_over_halves(l[w]);
+    if (!live[w]) continue;
     if (direct) {
-      if (a.lse) a.lse[flat] = l == 0.f ? -INFINITY : (m - kWideShift + __log2f(l)) * 0.6931471805599453f;
+      typedef elem vec4 __attribute__((ext_vector_type(4)));
+      const float inv = sum == 0.f ? 0.f : 1.0f / sum;
+      elem *dst = static_cast<elem *>(a.out) + flat[w] * D + 4 * h;
+#pragma unroll
+      for (int i = 0; i < kDT; ++i)
+#pragma unroll
+        for (int r = 0; r < 16; r += 4)
+          *reinterpret_cast<vec4 *>(dst + 32 * i + 2 * r) =
+              vec4{(elem)(o[w][i][r] * inv), (elem)(o[w][i][r + 1] * inv),
+                   (elem)(o[w][i][r + 2] * inv), (elem)(o[w][i][r + 3] * inv)};
+      if (h == 0 && a.lse)
+        a.lse[flat[w]] = sum == 0.f ? -INFINITY : (m[w] - kWideShift + __log2f(sum)) * 0.6931471805599453f;
     } else {
-      a.part_ml[it.part * nrows + flat] = make_float2(m - kWideShift, l);
+      float *dst = a.part_o + (it.part * nrows + flat[w]) * D + 4 * h;
+#pragma unroll
+      for (int i = 0; i < kDT; ++i)
+#pragma unroll
+        for (int r = 0; r < 16; r += 4)
+          *reinterpret_cast<float4_t *>(dst + 32 * i + 2 * r) =
+              float4_t{o[w][i][r], o[w][i][r + 1], o[w][i][r + 2], o[w][i][r + 3]};
+      if (h == 0) a.part_ml[it.part * nrows + flat[w]] = make_float2(m[w] - kWideShift, sum);
     }
   }
+}
+
+template <class T, int D, int NW, int R>
+__global__ void __launch_bounds__(64 * NW, wide_waves(D, NW, R))
+attn_wide_kernel(AttnPrefix a, uint32_t item0) {
+  extern __shared__ __attribute__((aligned(16))) uint8_t smem[];
+  Item it;
+  if (find_item(a, item0 + spread(blockIdx.x, gridDim.x), 32 * R * NW, it))
+    wide_body<T, D, NW, R>(a, it, smem);
 }
 
 // Joins the partial results of each row: D / 4 threads a row, four
@@ -557,17 +744,20 @@ attn_join_kernel(AttnPrefix a) {
   if (threadIdx.x / kPer >= kRowsPerBlock || row >= nrows) return;
   const int parts = a.prefix_parts + a.suffix_parts;
   float m = -INFINITY;
+#pragma unroll 4
   for (int p = 0; p < parts; ++p) m = fmaxf(m, a.part_ml[p * nrows + row].x);
   float l = 0.f;
   float4_t o = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 4
   for (int p = 0; p < parts; ++p) {
+    // a part that sees no key has m = -inf: nothing of it counts
     const float2 ml = a.part_ml[p * nrows + row];
-    if (ml.x == -INFINITY) continue;  // no key of this part is seen
-    const float w = __builtin_amdgcn_exp2f(ml.x - m);
     const float4_t x = *reinterpret_cast<const float4_t *>(a.part_o + (p * nrows + row) * D + d);
-    l += w * ml.y;
+    const bool seen = ml.x != -INFINITY;
+    const float w = seen ? __builtin_amdgcn_exp2f(ml.x - m) : 0.f;
+    l += w * (seen ? ml.y : 0.f);
 #pragma unroll
-    for (int r = 0; r < 4; ++r) o[r] += w * x[r];
+    for (int r = 0; r < 4; ++r) o[r] += w * (seen ? x[r] : 0.f);
   }
   const float inv = l == 0.f ? 0.f : 1.0f / l;
   elem *dst = static_cast<elem *>(a.out) + row * D + d;
@@ -577,26 +767,38 @@ attn_join_kernel(AttnPrefix a) {
     a.lse[row] = l == 0.f ? -INFINITY : (m + __log2f(l)) * 0.6931471805599453f;
 }
 
-template <class T, int D, int NW>
+template <class T, int D, int NW, int R>
 hipError_t launch_wide(const AttnPrefix &a, int64_t item0, int64_t items, hipStream_t stream) {
-  constexpr auto kern = attn_wide_kernel<T, D, NW>;
+  constexpr auto kern = attn_wide_kernel<T, D, NW, R>;
   const hipError_t e = ensure_max_lds<kern>(Wide<D>::kLds);
   if (e != hipSuccess) return e;
-  hipLaunchKernelGGL(kern, dim3((unsigned)items), dim3(64 * NW), Wide<D>::kLds, stream, a, (uint32_t)item0);
+  hipLaunchKernelGGL(kern, dim3((unsigned)items), dim3(64 * NW), Wide<D>::kLds, stream, a,
+                     (uint32_t)item0);
   return hipGetLastError();
 }
 
+// Workgroups of 256 rows are eight waves of 32, or four of 64 where the
+// registers leave room for two such waves a SIMD. Measured (us): 768 rows x
+// 32801 keys x 8 heads of 128 bf16 118 / 145; chunks of 11160 rows x 8200
+// keys x 4 heads of 64 fp16 210 / 183.
 template <class T, int D>
 hipError_t launch_items(const AttnPrefix &a, int wide, int64_t item0, int64_t items,
                         hipStream_t stream) {
   if (items == 0) return hipSuccess;
-  if (wide == 8) return launch_wide<T, D, D == 64 || D == 128 ? 8 : 4>(a, item0, items, stream);
-  if (wide == 4) return launch_wide<T, D, 4>(a, item0, items, stream);
+  if (wide == 2) {
+    if constexpr (D == 128) return launch_wide<T, D, 8, 1>(a, item0, items, stream);
+    if constexpr (D < 128) return launch_wide<T, D, 4, 2>(a, item0, items, stream);
+    return hipErrorInvalidValue;
+  }
+  if (wide == 1) return launch_wide<T, D, 4, 1>(a, item0, items, stream);
   hipLaunchKernelGGL((attn_rows16_kernel<T, D>), dim3((unsigned)items), dim3(kThreads), 0, stream, a,
                      (uint32_t)item0);
   return hipGetLastError();
 }
 
+// The prefix's and the suffixes' items are launched together when they are of
+// one kind. (16-row items in the wide kernel's launch measured no faster: its
+// LDS leaves them one workgroup a CU, and they need several to cover memory.)
 template <class T, int D>
 hipError_t launch(const AttnPrefix &a, hipStream_t stream) {
   hipError_t e;
@@ -632,14 +834,14 @@ hipError_t launch_dim(const AttnPrefix &a, hipStream_t stream) {
 // Splits the keys so that the launch fills the chip. A chunk is a multiple of
 // 128 keys and at most kAttnMaxChunk.
 void attn_prefix_plan(AttnPrefix &a, int64_t max_suffix, int num_cus) {
-  // Waves of the wide kernel for `rows` rows, 0 for the 16-row kernel.
+  // Rows of a work item: 16 (up to 32 rows, where reading the cache is the
+  // cost), or 128 * wide of the wide kernel.
   auto wide_for = [&](int64_t rows) {
     if (rows <= 32) return 0;
-    return rows > 128 && (a.head_dim == 64 || a.head_dim == 128) ? 8 : 4;
+    return rows > 128 && a.head_dim <= 128 ? 2 : 1;
   };
-  // Chunk for `keys` keys of `blocks` row blocks. The 16-row kernel runs
-  // several workgroups on a CU; the wide one runs one, so its number of
-  // chunks is chosen for whole rounds of the CUs.
+  // Chunk for `keys` keys of `blocks` row blocks: several 16-row workgroups
+  // for each CU; for the wide kernel whole rounds over the CUs.
   auto chunk_of = [&](int64_t keys, int64_t blocks, int wide) {
     const int64_t most = (keys + 127) / 128;
     int64_t parts = (4 * (int64_t)num_cus + blocks - 1) / blocks;
@@ -661,7 +863,7 @@ void attn_prefix_plan(AttnPrefix &a, int64_t max_suffix, int num_cus) {
     if (chunk > kAttnMaxChunk) chunk = kAttnMaxChunk;
     return (int)chunk;
   };
-  auto block_rows = [](int wide) { return wide ? 32 * wide : kRows; };
+  auto block_rows = [](int wide) { return wide ? 128 * wide : kRows; };
   a.group = a.n_q_heads / a.n_kv_heads;
   const int64_t prefix_rows = a.tokens * a.group, suffix_rows = a.max_q * a.group;
   a.prefix_wide = wide_for(prefix_rows);

@@ -180,7 +180,7 @@ struct AttnPrefix {
   // plan (attn_prefix_plan)
   int group, prefix_row_blocks, prefix_chunk, prefix_parts;
   int suffix_row_blocks, suffix_chunk, suffix_parts;
-  int prefix_wide, suffix_wide;  // waves of the wide kernel's workgroups (0: 16-row kernel)
+  int prefix_wide, suffix_wide;  // 32-row tiles of a wave of the wide kernel (0: 16-row kernel)
   int64_t prefix_items, suffix_items;
   float *part_o;    // parts x (tokens x heads) x head_dim
   float2 *part_ml;  // parts x (tokens x heads): reference, sum
