@@ -19,7 +19,6 @@ The shared library is loaded on first use; if it has not been built
 from __future__ import annotations
 
 import ctypes
-import functools
 import os
 
 __all__ = [
@@ -390,87 +389,41 @@ def lqmm_gemv_i4g32(Wq, scales, zeros, x, N, out=None, workspace=None, stream=No
 # ---- serving operators ---------------------------------------------------------
 
 # A call's host time is part of a decode step (these calls take a few
-# microseconds on the GPU), so the bindings below look torch up once, read the
-# device and the stream as plain integers, and switch devices only when the
-# tensors are not on the current one.
-class _Torch:
-    torch = None
+# microseconds on the GPU), so their checks and the library call are native:
+# csrc/serve_binding.cpp, module _serve, set up on first use.
+_native = None
 
 
-def _serve():
-    """torch and the library, set up on first use."""
-    if _Torch.torch is None:
+def _calls():
+    global _native
+    if _native is None:
         torch = _torch()
-        _Torch.lib = load()
-        _Torch.f32, _Torch.f8, _Torch.u8 = torch.float32, torch.float8_e4m3fn, torch.uint8
-        _Torch.i32, _Torch.i64 = torch.int32, torch.int64
-        _Torch.codes = {torch.float32: 0, torch.float16: 1, torch.bfloat16: 2}
-        _Torch.get_device, _Torch.raw_stream = torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream
-        _Torch.torch = torch
-    return _Torch
+        load()
+        path = os.path.join(_HERE, "_serve.so")
+        if not os.path.exists(path):
+            raise RuntimeError(
+                f"_serve.so not found at {path}; build it with "
+                "`python -m block_quantized_matmul_amd.build` (there is no fallback path)")
+        from . import _serve as module  # (the compiled module)
+        module.setup(_check, torch._C._cuda_getCurrentRawStream, _scratch_for)
+        _native = module
+    return _native
 
 
-def _index_of(*ts):
-    """The device that all tensors are on, as an index."""
-    d = ts[0].get_device()
-    for t in ts:
-        if t.get_device() != d:
-            raise ValueError("all tensors must be on the same device")
-    return d
+# Scratch for attention's partial results when the caller passes no workspace:
+# one buffer per (device, stream), at least doubled when it grows. A buffer
+# that was outgrown is kept (they add up to less than the newest): launches in
+# flight and captured graphs may still use it.
+_scratch = {}
 
 
-def _call(index, stream, fn, *args):
-    """fn(*args, stream) on device ``index``."""
-    T = _Torch
-    if stream is None:
-        stream = T.raw_stream(index)
-    elif not isinstance(stream, int):
-        stream = stream.cuda_stream
-    if T.get_device() == index:
-        status = fn(*args, stream)
-    else:
-        with T.torch.cuda.device(index):
-            status = fn(*args, stream)
-    if status:
-        _check(status)
-
-
-def _type_code(dtype, name, allowed):
-    """lqmm_type value of a torch dtype."""
-    code = _Torch.codes.get(dtype)
-    if code not in allowed:
-        raise TypeError(f"{name} has element type {dtype}, which this call does not take")
-    return code
-
-
-def _rows(t, heads, dim, name):
-    """(tokens, heads, dim) with contiguous rows: its row stride in elements."""
-    if not isinstance(t, _Torch.torch.Tensor):
-        raise TypeError(f"{name} must be a torch.Tensor")
-    if not t.is_cuda:
-        raise ValueError(f"{name} must be a device tensor")
-    shape, s = t.shape, t.stride()
-    if len(shape) != 3 or shape[1] != heads or shape[2] != dim:
-        raise ValueError(f"{name} must be (tokens, {heads}, {dim}), got {tuple(shape)}")
-    if s[2] != 1 or (heads > 1 and s[1] != dim):
-        raise ValueError(f"the heads of one token of {name} must be contiguous")
-    return s[0] if shape[0] > 1 else heads * dim
-
-
-def _cache(k_cache, v_cache):
-    """Checks the two caches; (num_pages, n_kv_heads, page_size, head_dim, type)."""
-    if not isinstance(k_cache, _Torch.torch.Tensor):
-        raise TypeError("k_cache must be a torch.Tensor")
-    dtype = k_cache.dtype
-    _dev_tensor(k_cache, dtype, "k_cache")
-    _dev_tensor(v_cache, dtype, "v_cache")
-    shape = k_cache.shape
-    if len(shape) != 4:
-        raise ValueError("k_cache must be (num_pages, n_kv_heads, page_size, head_dim)")
-    pages, hkv, ps, d = shape
-    if ps % 8 or v_cache.shape != (pages, hkv, ps // 8, d, 8):
-        raise ValueError("v_cache must be (num_pages, n_kv_heads, page_size / 8, head_dim, 8)")
-    return pages, hkv, ps, d, _type_code(dtype, "k_cache", (1, 2))
+def _scratch_for(index, stream_handle, nbytes):
+    torch = _torch()
+    bufs = _scratch.setdefault((index, stream_handle), [])
+    if not bufs or bufs[-1].numel() < nbytes:
+        grown = max(nbytes, 2 * bufs[-1].numel() if bufs else 1 << 20)
+        bufs.append(torch.empty(grown, dtype=torch.uint8, device=torch.device("cuda", index)))
+    return bufs[-1]
 
 
 def kv_cache_empty(num_pages, n_kv_heads, page_size, head_dim, dtype=None, device="cuda"):
@@ -504,46 +457,8 @@ def lqmm_kv_append(q, k, v, positions, slots, k_cache, v_cache, rope_turns=None,
     Returns the rotated q in the caches' type (q may be None: returns None).
     positions: int32; rope_turns: the table of lqmm_rope_turns, None rotates
     nothing."""
-    T = _serve()
-    pages, hkv, ps, d, ctype = _cache(k_cache, v_cache)
-    ldk, ldv = _rows(k, hkv, d, "k"), _rows(v, hkv, d, "v")
-    tokens, dtype = k.shape[0], k.dtype
-    itype = _type_code(dtype, "k", (0, 1, 2))
-    if v.dtype != dtype or v.shape[0] != tokens:
-        raise ValueError("k and v must have the same element type and tokens")
-    _dev_tensor(slots, T.i64, "slots")
-    if slots.numel() != tokens:
-        raise ValueError(f"slots must have {tokens} entries")
-    index = _index_of(k, v, slots, k_cache, v_cache)
-    rot, pos_ptr, turns_ptr = 0, None, None
-    if rope_turns is not None:
-        _dev_tensor(rope_turns, T.i64, "rope_turns")
-        _dev_tensor(positions, T.i32, "positions")
-        if positions.numel() != tokens:
-            raise ValueError(f"positions must have {tokens} entries")
-        rot, pos_ptr, turns_ptr = 2 * rope_turns.numel(), positions.data_ptr(), rope_turns.data_ptr()
-        _index_of(k, rope_turns, positions)
-    hq, ldq, q_ptr, out_ptr = 0, 0, None, None
-    if q is not None:
-        if not isinstance(q, T.torch.Tensor) or q.dim() != 3:
-            raise ValueError("q must be (tokens, n_q_heads, head_dim)")
-        hq = q.shape[1]
-        ldq = _rows(q, hq, d, "q")
-        if q.dtype != dtype or q.shape[0] != tokens:
-            raise ValueError("q and k must have the same element type and tokens")
-        if q_out is None:
-            q_out = T.torch.empty((tokens, hq, d), dtype=k_cache.dtype, device=k_cache.device)
-        _dev_tensor(q_out, k_cache.dtype, "q_out")
-        if q_out.shape != (tokens, hq, d):
-            raise ValueError("q_out has the wrong shape")
-        q_ptr, out_ptr = q.data_ptr(), q_out.data_ptr()
-        _index_of(k, q, q_out)
-    elif q_out is not None:
-        raise ValueError("q_out without q")
-    _call(index, stream, T.lib.lqmm_kv_append, q_ptr, k.data_ptr(), v.data_ptr(), itype, ldq, ldk,
-          ldv, pos_ptr, slots.data_ptr(), turns_ptr, rot, 1 if interleaved else 0, out_ptr,
-          k_cache.data_ptr(), v_cache.data_ptr(), ctype, tokens, hq, hkv, d, ps, pages)
-    return q_out
+    return _calls().kv_append(q, k, v, positions, slots, k_cache, v_cache, rope_turns, interleaved,
+                              q_out, stream)
 
 
 def lqmm_attn_prefix_workspace_bytes(prefix_len, max_pages, max_q, tokens, batch, n_q_heads,
@@ -551,22 +466,6 @@ def lqmm_attn_prefix_workspace_bytes(prefix_len, max_pages, max_q, tokens, batch
     return load().lqmm_attn_prefix_workspace_bytes(
         int(prefix_len), int(max_pages), int(max_q), int(tokens), int(batch), int(n_q_heads),
         int(n_kv_heads), int(head_dim), int(page_size))
-
-
-# Scratch for partial results when the caller passes no workspace: one buffer
-# per (device, stream), at least doubled when it grows. A buffer that was
-# outgrown is kept (they add up to less than the newest): launches in flight
-# and captured graphs may still use it.
-_scratch = {}
-
-
-def _scratch_for(index, stream_handle, nbytes):
-    torch = _Torch.torch
-    bufs = _scratch.setdefault((index, stream_handle), [])
-    if not bufs or bufs[-1].numel() < nbytes:
-        grown = max(nbytes, 2 * bufs[-1].numel() if bufs else 1 << 20)
-        bufs.append(torch.empty(grown, dtype=torch.uint8, device=torch.device("cuda", index)))
-    return bufs[-1]
 
 
 def lqmm_attn_prefix(q, k_cache, v_cache, pages, seq_lens, prefix_pages=None, prefix_len=0,
@@ -580,125 +479,15 @@ def lqmm_attn_prefix(q, k_cache, v_cache, pages, seq_lens, prefix_pages=None, pr
     most ``max_q`` of them. scale: 1 / sqrt(head_dim) when None. Returns out
     (tokens, n_q_heads, head_dim), or (out, lse) with lse (tokens, n_q_heads)
     float32 when return_lse is set or lse is given."""
-    T = _serve()
-    npages, hkv, ps, d, ctype = _cache(k_cache, v_cache)
-    if not isinstance(q, T.torch.Tensor) or q.dim() != 3:
-        raise ValueError("q must be (tokens, n_q_heads, head_dim)")
-    tokens, hq, _ = q.shape
-    ldq = _rows(q, hq, d, "q")
-    dtype = q.dtype
-    if dtype != k_cache.dtype:
-        raise TypeError("q must have the caches' element type")
-    _dev_tensor(pages, T.i32, "pages")
-    _dev_tensor(seq_lens, T.i32, "seq_lens")
-    if pages.dim() != 2 or seq_lens.dim() != 1 or pages.shape[0] != seq_lens.shape[0]:
-        raise ValueError("pages must be (batch, max_pages) and seq_lens (batch,)")
-    batch, max_pages = pages.shape
-    index = _index_of(q, k_cache, v_cache, pages, seq_lens)
-    start_ptr = prefix_ptr = lse_ptr = ws_ptr = None
-    if q_start is not None:
-        _dev_tensor(q_start, T.i32, "q_start")
-        if q_start.numel() != batch + 1:
-            raise ValueError(f"q_start must have {batch + 1} entries")
-        _index_of(q, q_start)
-        start_ptr = q_start.data_ptr()
-    prefix_len, max_q, ws_bytes = int(prefix_len), int(max_q), 0
-    if prefix_len:
-        _dev_tensor(prefix_pages, T.i32, "prefix_pages")
-        if prefix_pages.numel() * ps < prefix_len:
-            raise ValueError("prefix_pages hold fewer than prefix_len tokens")
-        _index_of(q, prefix_pages)
-        prefix_ptr = prefix_pages.data_ptr()
-    if out is None:
-        out = T.torch.empty((tokens, hq, d), dtype=dtype, device=q.device)
-    else:
-        _dev_tensor(out, dtype, "out")
-        if out.shape != (tokens, hq, d):
-            raise ValueError("out has the wrong shape")
-        _index_of(q, out)
-    if lse is not None:
-        _dev_tensor(lse, T.f32, "lse")
-        if lse.numel() != tokens * hq:
-            raise ValueError("lse has the wrong size")
-        _index_of(q, lse)
-    elif return_lse:
-        lse = T.torch.empty((tokens, hq), dtype=T.f32, device=q.device)
-    if lse is not None:
-        lse_ptr = lse.data_ptr()
-    if scale is None:
-        scale = d ** -0.5
-    if stream is None:
-        stream = T.raw_stream(index)
-    elif not isinstance(stream, int):
-        stream = stream.cuda_stream
-    if workspace is None:
-        need = _attn_need(index, prefix_len, max_pages, max_q, tokens, batch, hq, hkv, d, ps)
-        if need:
-            workspace = _scratch_for(index, stream, need)
-            ws_ptr, ws_bytes = workspace.data_ptr(), workspace.numel()
-    else:
-        _dev_tensor(workspace, T.u8, "workspace")
-        _index_of(q, workspace)
-        ws_ptr, ws_bytes = workspace.data_ptr(), workspace.numel()
-    _call(index, stream, T.lib.lqmm_attn_prefix, q.data_ptr(), ldq, k_cache.data_ptr(),
-          v_cache.data_ptr(), ctype, prefix_ptr, prefix_len, pages.data_ptr(), max_pages,
-          seq_lens.data_ptr(), start_ptr, max_q, out.data_ptr(), lse_ptr, scale, tokens, batch, hq,
-          hkv, d, ps, npages, ws_ptr, ws_bytes)
-    return (out, lse) if lse is not None else out
-
-
-@functools.lru_cache(maxsize=4096)
-def _attn_need(index, *sizes):
-    """lqmm_attn_prefix_workspace_bytes on device ``index`` (a function of the
-    sizes alone, asked for every decode step)."""
-    with _Torch.torch.cuda.device(index):
-        return _Torch.lib.lqmm_attn_prefix_workspace_bytes(*sizes)
-
-
-def _codes(t, name):
-    """A 2-D contiguous tensor of e4m3 codes (float8_e4m3fn or raw uint8)."""
-    T = _Torch
-    if not isinstance(t, T.torch.Tensor) or t.dtype not in (T.f8, T.u8):
-        raise TypeError(f"{name} must be a float8_e4m3fn (or uint8) torch.Tensor")
-    _dev_tensor(t, t.dtype, name)
-    if t.dim() != 2:
-        raise ValueError(f"{name} must be 2-D")
-    return t
+    return _calls().attn_prefix(q, k_cache, v_cache, pages, seq_lens, prefix_pages, prefix_len,
+                                q_start, max_q, scale, out, return_lse, lse, workspace, stream)
 
 
 def lqmm_quant_f8b128(X, out=None, scales=None, stream=None):
     """X (M, K) float32, float16 or bfloat16 (rows may be strided) to e4m3 codes
     with a scale per row and 128 columns: (codes (M, K) float8_e4m3fn, scales
     (ceil(K / 128), M) float32)."""
-    T = _serve()
-    if not isinstance(X, T.torch.Tensor) or X.dim() != 2:
-        raise ValueError("X must be (M, K)")
-    if not X.is_cuda:
-        raise ValueError("X must be a device tensor")
-    M, K = X.shape
-    ld, s1 = X.stride()
-    if K > 1 and s1 != 1:
-        raise ValueError("the rows of X must be contiguous")
-    xtype = _type_code(X.dtype, "X", (0, 1, 2))
-    blocks = (K + 127) // 128
-    index = X.get_device()
-    if out is None:
-        out = T.torch.empty((M, K), dtype=T.f8, device=X.device)
-    else:
-        _codes(out, "out")
-        if out.shape != (M, K):
-            raise ValueError("out has the wrong shape")
-        _index_of(X, out)
-    if scales is None:
-        scales = T.torch.empty((blocks, M), dtype=T.f32, device=X.device)
-    else:
-        _dev_tensor(scales, T.f32, "scales")
-        if scales.shape != (blocks, M):
-            raise ValueError("scales has the wrong shape")
-        _index_of(X, scales)
-    _call(index, stream, T.lib.lqmm_quant_f8b128, X.data_ptr(), xtype, ld if M > 1 else K,
-          out.data_ptr(), scales.data_ptr(), M, K)
-    return out, scales
+    return _calls().quant_f8b128(X, out, scales, stream)
 
 
 def lqmm_gemm_f8b128(W, wscale, Xq, xscale, out=None, out_dtype=None, stream=None):
@@ -706,25 +495,4 @@ def lqmm_gemm_f8b128(W, wscale, Xq, xscale, out=None, out_dtype=None, stream=Non
     with wscale (ceil(N / 128), ceil(K / 128)), Xq (M, K) with xscale
     (ceil(K / 128), M) as lqmm_quant_f8b128 makes them. out_dtype: float16
     (default), bfloat16 or float32."""
-    T = _serve()
-    _codes(W, "W")
-    _codes(Xq, "Xq")
-    _dev_tensor(wscale, T.f32, "wscale")
-    _dev_tensor(xscale, T.f32, "xscale")
-    (N, K), (M, K2) = W.shape, Xq.shape
-    if K2 != K:
-        raise ValueError(f"shape mismatch: W {tuple(W.shape)} Xq {tuple(Xq.shape)}")
-    blocks = (K + 127) // 128
-    if wscale.shape != ((N + 127) // 128, blocks) or xscale.shape != (blocks, M):
-        raise ValueError("wscale or xscale has the wrong shape")
-    if out is None:
-        out = T.torch.empty((M, N), dtype=out_dtype or T.torch.float16, device=W.device)
-    else:
-        _dev_tensor(out, out_dtype or out.dtype, "out")
-        if out.shape != (M, N):
-            raise ValueError("out has the wrong shape")
-    ytype = _type_code(out.dtype, "out", (0, 1, 2))
-    index = _index_of(W, wscale, Xq, xscale, out)
-    _call(index, stream, T.lib.lqmm_gemm_f8b128, W.data_ptr(), wscale.data_ptr(), Xq.data_ptr(),
-          xscale.data_ptr(), out.data_ptr(), ytype, M, N, K)
-    return out
+    return _calls().gemm_f8b128(W, wscale, Xq, xscale, out, out_dtype, stream)

@@ -1,5 +1,6 @@
 """Build liblqmm.so (HIP, gfx950) in-tree with hipcc, and the benchmark's
-streaming-read probe (liblqmm_probe.so).
+streaming-read probe (liblqmm_probe.so), and the native Python calls of the
+serving operators (_serve.so, against torch's headers).
 
 Each source is compiled to an object in parallel, then the objects are linked
 into the shared library.
@@ -23,6 +24,9 @@ SOURCES = ["api.hip", "gemv.hip", "gemv_small.hip", "gemv_small_more.hip", "gemm
            "attn_prefix.hip", "f8b128.hip"]
 PROBE_LIB = os.path.join(HERE, "liblqmm_probe.so")
 PROBE_SOURCES = ["probe.hip"]
+BINDING = os.path.join(HERE, "_serve.so")
+BINDING_SOURCE = "serve_binding.cpp"
+CXX = os.environ.get("CXX", "g++")
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 FLAGS = [
@@ -40,7 +44,7 @@ def _run(cmd, what, verbose):
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         sys.stderr.write(r.stdout + r.stderr)
-        raise RuntimeError(f"hipcc failed building {what}")
+        raise RuntimeError(f"{os.path.basename(cmd[0])} failed building {what}")
     err = "\n".join(l for l in r.stderr.splitlines() if "packed-fp32-ops" not in l
                     and "not a recognized feature" not in l)
     if verbose and err.strip():
@@ -62,9 +66,29 @@ def _hipcc(sources, lib, verbose):
     return lib
 
 
+def _binding(verbose):
+    import sysconfig
+
+    import torch
+    root = os.path.dirname(torch.__file__)
+    tmp = BINDING + ".tmp"
+    _run([CXX, "-O2", "-std=c++17", "-fPIC", "-shared", "-Wall",
+          f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+          "-I", os.path.join(ROOT, "include"), "-I", sysconfig.get_paths()["include"],
+          "-isystem", os.path.join(root, "include"),
+          "-isystem", os.path.join(root, "include", "torch", "csrc", "api", "include"),
+          os.path.join(CSRC, BINDING_SOURCE), "-o", tmp,
+          "-L", HERE, "-l:" + os.path.basename(LIB), "-Wl,-rpath,$ORIGIN",
+          "-L", os.path.join(root, "lib"), "-ltorch_python", "-ltorch_cpu", "-ltorch", "-lc10"],
+         BINDING_SOURCE, verbose)
+    os.replace(tmp, BINDING)
+
+
 def build(verbose: bool = False) -> str:
     _hipcc(PROBE_SOURCES, PROBE_LIB, verbose)
-    return _hipcc(SOURCES, LIB, verbose)
+    lib = _hipcc(SOURCES, LIB, verbose)
+    _binding(verbose)
+    return lib
 
 
 if __name__ == "__main__":
