@@ -335,21 +335,22 @@ template <class T, bool F8, int TM, int TN, int DEPTH>
 __global__ void __launch_bounds__(64 * kRowWaves)
 gemm_f8b128_rows_kernel(const uint8_t *__restrict__ W, const float *__restrict__ sw,
                         const uint8_t *__restrict__ X, const float *__restrict__ sx,
-                        typename T::elem *__restrict__ Y, int M, int64_t N, int64_t K) {
+                        typename T::elem *__restrict__ Y, int64_t M, int64_t N, int64_t K,
+                        uint32_t tiles_n) {
   constexpr int kN = 16 * TN, kM = 16 * TM, kLd = kN + 4;
   __shared__ __attribute__((aligned(16))) float part[kRowWaves][kM][kLd];
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int l16 = lane & 15, g = lane >> 4;
-  const int64_t n0 = (int64_t)blockIdx.x * kN;
-  const int m0 = blockIdx.y * kM;
+  const int64_t n0 = (int64_t)(blockIdx.x % tiles_n) * kN;
+  const int64_t m0 = (int64_t)(blockIdx.x / tiles_n) * kM;
   const int blocks = (int)((K + BK - 1) / BK);
   const int per = (blocks + kRowWaves - 1) / kRowWaves;
   const int kb0 = wave * per, kb1 = kb0 + per < blocks ? kb0 + per : blocks;
   const uint32_t Ku = (uint32_t)K;
 
   const int64_t wrows = N - n0 < kN ? N - n0 : kN;
-  const int xrows = M - m0 < kM ? M - m0 : kM;
+  const int xrows = (int)(M - m0 < kM ? M - m0 : kM);
   // rows past the ends read zeros
   const rsrc_t wr = make_rsrc(W + n0 * K, (uint32_t)(wrows * K));
   const rsrc_t xr = make_rsrc(X + m0 * K, (uint32_t)(xrows * K));
@@ -437,7 +438,7 @@ gemm_f8b128_rows_kernel(const uint8_t *__restrict__ W, const float *__restrict__
     float y = 0.f;
 #pragma unroll
     for (int w = 0; w < kRowWaves; ++w) y += part[w][m][n];
-    Y[(int64_t)(m0 + m) * N + n0 + n] = (typename T::elem)y;
+    Y[(m0 + m) * N + n0 + n] = (typename T::elem)y;
   }
 }
 
@@ -458,12 +459,11 @@ hipError_t launch_tile(const uint8_t *W, const float *sw, const uint8_t *X, cons
 template <class T, int TM, int TN, int DEPTH>
 hipError_t launch_rows(const uint8_t *W, const float *sw, const uint8_t *X, const float *sx, void *Y,
                        int64_t M, int64_t N, int64_t K, hipStream_t stream) {
-  const int64_t grid = (N + 16 * TN - 1) / (16 * TN);
-  if (grid > 0x7fffffff) return hipErrorInvalidValue;
+  const int64_t tn = (N + 16 * TN - 1) / (16 * TN), tm = (M + 16 * TM - 1) / (16 * TM);
+  if (tm * tn > 0x7fffffff) return hipErrorInvalidValue;
   hipLaunchKernelGGL((gemm_f8b128_rows_kernel<T, __is_same(T, TypeBF16), TM, TN, DEPTH>),
-                     dim3((unsigned)grid, (unsigned)((M + 16 * TM - 1) / (16 * TM))),
-                     dim3(64 * kRowWaves), 0, stream, W, sw, X, sx,
-                     static_cast<typename T::elem *>(Y), (int)M, N, K);
+                     dim3((unsigned)(tm * tn)), dim3(64 * kRowWaves), 0, stream, W, sw, X, sx,
+                     static_cast<typename T::elem *>(Y), M, N, K, (uint32_t)tn);
   return hipGetLastError();
 }
 
@@ -479,42 +479,51 @@ hipError_t launch_gemm(const uint8_t *W, const float *sw, const uint8_t *X, cons
       return launch_rows<T, 1, 4, 2>(W, sw, X, sx, Y, M, N, K, stream);
     return launch_rows<T, 1, 1, 4>(W, sw, X, sx, Y, M, N, K, stream);
   }
-  // Up to 32 rows and one workgroup a CU, the same: M = 32, N = 4096 9.2
-  // against 12.1 for the tiles below, N = 7000 14.4 against 10.7.
-  if (M <= 32 && N <= 16 * (int64_t)num_cus)
-    return launch_rows<T, 2, 1, 2>(W, sw, X, sx, Y, M, N, K, stream);
-
-  // Tiles: the one whose rounds over the CUs cost least. Cost of a round per
-  // scale block, measured at K = 4096 (ns; f8 cores / fp16 cores).
+  // Else the kernel and tile whose estimated time is least: rounds over the
+  // CUs times what a workgroup takes, a fixed part and one per scale block.
+  // The two parts (ns; the second for f8 / fp16 cores) were fitted to times
+  // at M = 24 .. 4096, N = 1001 .. 14336, K = 1040 and 4096; e.g. (us) 24 x
+  // 4127 x 4096 10.1 with 32 x 32 rows and 11.6 with 64 x 32 tiles, 200 x 4127
+  // x 1040 14.2 with 64 x 32 rows, 17.1 with 64 x 32 and 12.6 with 64 x 64
+  // tiles, 512 x 14336 x 4096 44 with 128 x 256 and 60 with 256 x 256 tiles.
   constexpr bool F8 = __is_same(T, TypeBF16);
   struct Choice {
-    int bm, bn, per_cu, cost;
+    int bm, bn, per_cu, fixed, block;
   };
   constexpr Choice kChoices[] = {
-      {64, 32, 1, F8 ? 270 : 330},   {64, 64, 1, F8 ? 310 : 400},    {64, 64, 2, F8 ? 510 : 800},
-      {128, 128, 1, F8 ? 750 : 1100}, {128, 256, 1, F8 ? 1300 : 2050}, {256, 256, 1, F8 ? 2000 : 9999}};
-  int best = 0;
+      // W straight to registers, for few rows of X
+      {32, 16, 1, 200, 170}, {32, 32, 1, 200, 250}, {48, 32, 1, 200, 350}, {64, 32, 1, 200, 420},
+      // LDS tiles
+      {64, 32, 1, 2000, F8 ? 190 : 240}, {64, 64, 1, 3000, F8 ? 220 : 280},
+      {64, 64, 2, 2000, F8 ? 450 : 660}, {128, 128, 1, 3000, F8 ? 750 : 1100},
+      {128, 256, 1, 4000, F8 ? 1300 : 2050}, {256, 256, 1, 5000, F8 ? 2000 : 99999}};
+  const int64_t blocks = (K + BK - 1) / BK;
+  int best = -1;
   int64_t best_cost = 0;
-  for (int c = 0; c < 6; ++c) {
+  for (int c = 0; c < 10; ++c) {
     const Choice &o = kChoices[c];
     const int64_t tiles = ((M + o.bm - 1) / o.bm) * ((N + o.bn - 1) / o.bn);
     const int64_t slots = (int64_t)o.per_cu * num_cus;
-    const int64_t cost = (tiles + slots - 1) / slots * o.cost;
-    if (c == 0 || cost < best_cost) {
+    if (tiles > 0x7fffffff) continue;  // more workgroups than a launch takes
+    const int64_t cost = (tiles + slots - 1) / slots * (o.fixed + o.block * blocks);
+    if (best < 0 || cost < best_cost) {
       best = c;
       best_cost = cost;
     }
   }
   switch (best) {
-    case 0: return launch_tile<T, 64, 32, 1, 1, 4, 3>(W, sw, X, sx, Y, M, N, K, stream);
-    case 1: return launch_tile<T, 64, 64, 1, 2, 4, 2>(W, sw, X, sx, Y, M, N, K, stream);
-    case 2: return launch_tile<T, 64, 64, 1, 2, 2, 2>(W, sw, X, sx, Y, M, N, K, stream);
-    case 3: return launch_tile<T, 128, 128, 2, 2, 2, 2>(W, sw, X, sx, Y, M, N, K, stream);
-    case 4: return launch_tile<T, 128, 256, 2, 4, 1, 3>(W, sw, X, sx, Y, M, N, K, stream);
+    case 0: return launch_rows<T, 2, 1, 2>(W, sw, X, sx, Y, M, N, K, stream);
+    case 1: return launch_rows<T, 2, 2, 2>(W, sw, X, sx, Y, M, N, K, stream);
+    case 2: return launch_rows<T, 3, 2, 2>(W, sw, X, sx, Y, M, N, K, stream);
+    case 3: return launch_rows<T, 4, 2, 2>(W, sw, X, sx, Y, M, N, K, stream);
+    case 4: return launch_tile<T, 64, 32, 2, 1, 4, 3>(W, sw, X, sx, Y, M, N, K, stream);
+    case 5: return launch_tile<T, 64, 64, 1, 2, 4, 2>(W, sw, X, sx, Y, M, N, K, stream);
+    case 6: return launch_tile<T, 64, 64, 2, 2, 2, 2>(W, sw, X, sx, Y, M, N, K, stream);
+    case 7: return launch_tile<T, 128, 128, 2, 2, 2, 2>(W, sw, X, sx, Y, M, N, K, stream);
+    case 8: return launch_tile<T, 128, 256, 2, 4, 1, 3>(W, sw, X, sx, Y, M, N, K, stream);
   }
   // (fp16 cores: never the best, their operands do not fit beside 256 x 256 sums)
-  if constexpr (F8)
-    return launch_tile<T, 256, 256, 2, 4, 1, 2>(W, sw, X, sx, Y, M, N, K, stream);
+  if constexpr (F8) return launch_tile<T, 256, 256, 2, 4, 1, 2>(W, sw, X, sx, Y, M, N, K, stream);
   return hipErrorInvalidValue;
 }
 

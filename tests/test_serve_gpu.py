@@ -379,6 +379,8 @@ def test_f8_product(M, N, K, t):
     (700, 8300, 272, "f32"), (1500, 9000, 384, "bf16"), (1500, 9000, 256, "f16"),
     (2900, 9100, 400, "bf16"), (2900, 9100, 272, "f16"), (16, 12300, 144, "f16"),
     (9, 12301, 1040, "bf16"), (32, 4000, 2064, "f32"), (20, 300, 16, "bf16"),
+    (45, 4127, 4112, "f32"), (64, 3000, 1040, "f16"), (100, 1001, 272, "bf16"),
+    (2200000, 1, 16, "f16"), (1, 2200000, 16, "bf16"),
 ])
 def test_f8_product_large(M, N, K, t):
     """Every tile size, ends in all three directions; expected values in 64
