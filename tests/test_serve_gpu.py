@@ -322,6 +322,28 @@ def test_quant_codes(M, K, t):
     assert np.array_equal(np64(codes), want)
 
 
+def test_quant_every_quotient():
+    """Codes equal those of the correctly rounded quotient: random mantissas and
+    scales over the exponent range, and values on and next to the ties."""
+    r = np.random.default_rng(11)
+    x = r.standard_normal((4096, 1024)).astype(np.float32)
+    x *= np.exp2(r.integers(-60, 60, (4096, 8))).astype(np.float32).repeat(128, 1)
+    # ties of e4m3 times a group's scale, moved by at most one ulp
+    v = np.sort(np.unique(np.abs(so.E4M3[np.isfinite(so.E4M3)])))
+    mid = ((v[:-1] + v[1:]) / 2).astype(np.float32)
+    for m in range(0, 4096, 2):
+        top = np.float32(1 + r.random())
+        s = np.float32(top / np.float32(448.0))
+        t = (r.choice(mid, 127) * s).astype(np.float32)
+        t = np.nextafter(t, t + r.integers(-1, 2, 127).astype(np.float32) * np.float32(1e30)).astype(np.float32)
+        x[m, :127], x[m, 127] = np.clip(t, -top, top), top
+    announce("quant: every quotient")
+    codes, scales = bq.lqmm_quant_f8b128(torch.from_numpy(x).to(DEV))
+    want, ws = so.quantize(x)
+    assert np.array_equal(scales.cpu().numpy(), ws)
+    assert np.array_equal(np64(codes), want)
+
+
 def test_quant_strided_and_special():
     r = np.random.default_rng(3)
     x = rnd(r, (5, 400), "f16")
