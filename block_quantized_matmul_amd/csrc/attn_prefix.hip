@@ -840,11 +840,14 @@ void attn_prefix_plan(AttnPrefix &a, int64_t max_suffix, int num_cus) {
     if (rows <= 32) return 0;
     return rows > 128 && a.head_dim <= 128 ? 2 : 1;
   };
-  // Chunk for `keys` keys of `blocks` row blocks: several 16-row workgroups
-  // for each CU; for the wide kernel whole rounds over the CUs.
+  // Chunk for `keys` keys of `blocks` row blocks: as many chunks as give each
+  // CU a 16-row workgroup (one workgroup's four waves keep 64 KB of a CU's
+  // loads out; more chunks only add joins: 1 x 30001 keys, 8 key heads of 128
+  // fp16 34 us with one workgroup a CU, 39 with two, 49 with four; 24 x 4111,
+  // 32 heads 158 / 158 / 173); for the wide kernel whole rounds over the CUs.
   auto chunk_of = [&](int64_t keys, int64_t blocks, int wide) {
     const int64_t most = (keys + 127) / 128;
-    int64_t parts = (4 * (int64_t)num_cus + blocks - 1) / blocks;
+    int64_t parts = (num_cus + blocks - 1) / blocks;
     if (wide) {
       int64_t best = -1;
       for (int64_t p = 1; p <= most && p <= 64; ++p) {
