@@ -8,7 +8,8 @@ kernels; PyTorch provides device memory and streams only.
 
 The serving operators (the paged cache, attention with a shared prefix, 8-bit
 float products) take torch's float16, bfloat16, float32 and float8_e4m3fn
-tensors of the shapes given at each function.
+tensors of the shapes given at each function. Outputs that are not passed are
+allocated on the current stream: with another ``stream``, pass them.
 
 Weight tensors are flat ``torch.uint8`` device tensors (or 2-D, rows of
 packed blocks) holding the llama.cpp block bytes described in ``lqmm.h``.
@@ -423,6 +424,10 @@ def _scratch_for(index, stream_handle, nbytes):
     if not bufs or bufs[-1].numel() < nbytes:
         grown = max(nbytes, 2 * bufs[-1].numel() if bufs else 1 << 20)
         bufs.append(torch.empty(grown, dtype=torch.uint8, device=torch.device("cuda", index)))
+        # The memory may have been freed on the current stream a moment ago:
+        # nothing may still use it when another stream's launch writes it.
+        if not torch.cuda.is_current_stream_capturing():
+            torch.cuda.synchronize(index)
     return bufs[-1]
 
 

@@ -834,10 +834,13 @@ hipError_t launch_dim(const AttnPrefix &a, hipStream_t stream) {
 // Splits the keys so that the launch fills the chip. A chunk is a multiple of
 // 128 keys and at most kAttnMaxChunk.
 void attn_prefix_plan(AttnPrefix &a, int64_t max_suffix, int num_cus) {
-  // Rows of a work item: 16 (up to 32 rows, where reading the cache is the
-  // cost), or 128 * wide of the wide kernel.
+  // Rows of a work item: 16 while reading the cache is the cost, else 128 or
+  // 256 (wide 1, 2). Measured, a prefix of 16001 keys, 8 key heads, fp16 (us;
+  // 16-row / 128 / 256): 128 dimensions, 32 rows 29.5 / 33.6 / 35.3, 48 rows
+  // 37.3 / 34.5 / 36.2, 128 rows 81 / 38.1 / 40.5, 192 rows 148 / 45.7 / 45.2;
+  // 64 dimensions, 64 rows 27.3 / 28.7 / 31.8, 128 rows 45.7 / 31.1 / 34.1.
   auto wide_for = [&](int64_t rows) {
-    if (rows <= 32) return 0;
+    if (rows <= (a.head_dim == 64 ? 64 : 32)) return 0;
     return rows > 128 && a.head_dim <= 128 ? 2 : 1;
   };
   // Chunk for `keys` keys of `blocks` row blocks: as many chunks as give each
