@@ -121,6 +121,111 @@ __device__ __forceinline__ uint32_t spread(uint32_t block, uint32_t n) {
   return x * q + (x < r ? x : r) + block / 8;
 }
 
+// ---- values behind a mask -------------------------------------------------------
+// A masked weight is 0, and 0 times a value that is infinite or NaN is NaN: a
+// new token with such a value would reach the new tokens before it, whose mask
+// leaves it out, through the matrix products. That leaves NaN in O, which is
+// looked for once, behind the keys' loop; rows of a block that has such a
+// value among the keys of its mask's edge are done again, by themselves. (The
+// test at the end costs nothing that can be measured; the values' own test in
+// the loop would be done for every key of the edge.)
+template <class T, int D>
+__device__ __forceinline__ int64_t element_at(const AttnPrefix &a, const Item &it, int j) {
+  const int32_t p = it.pages[j >> a.page_log2];
+  const int64_t page = (uint32_t)p < (uint32_t)a.num_pages ? p : 0;
+  return ((page * a.n_kv_heads + it.h) * D << a.page_log2) +
+         (int64_t)(j & ((1 << a.page_log2) - 1)) * D;
+}
+
+// Whether V of the keys [from, it.c1) has a value that is not finite (one wave).
+template <class T, int D>
+__device__ __forceinline__ bool edge_not_finite(const AttnPrefix &a, const Item &it, int from) {
+  typedef typename T::vec8 vec8;
+  const int lane = threadIdx.x & 63;
+  const typename T::elem *vc = static_cast<const typename T::elem *>(a.v_cache);
+  if (from < it.c0) from = it.c0;
+  bool found = false;
+#pragma unroll 1
+  for (int j0 = from & ~7; j0 < it.c1; j0 += 8) {
+    const int64_t at = element_at<T, D>(a, it, j0);
+    for (int d = lane; d < D; d += 64) {
+      const vec8 x = *reinterpret_cast<const vec8 *>(vc + at + 8 * d);
+#pragma unroll
+      for (int e = 0; e < 8; ++e)
+        found = found || (j0 + e >= from && j0 + e < it.c1 && !(fabsf((float)x[e]) < INFINITY));
+    }
+  }
+  return __any(found);
+}
+
+// One row of an item by one wave: a lane a key for the logits, a lane a
+// dimension for O, only of keys that the row sees.
+template <class T, int D>
+__device__ __forceinline__ void row_alone(const AttnPrefix &a, const Item &it, int row) {
+  typedef typename T::elem elem;
+  constexpr int kO = (D + 63) / 64;
+  const int lane = threadIdx.x & 63, G = a.group;
+  const int tok = row / G;
+  const int64_t flat = (it.tok0 + tok) * a.n_q_heads + it.h * G + row % G;
+  const int limit = it.past + it.per_token * tok;
+  const int end = limit < it.c1 ? limit : it.c1;
+  const elem *q = static_cast<const elem *>(a.q) + (it.tok0 + tok) * a.ldq + (int64_t)(it.h * G + row % G) * D;
+  const elem *kc = static_cast<const elem *>(a.k_cache), *vc = static_cast<const elem *>(a.v_cache);
+  const float scale = a.q_sign ? -a.scale_log2 : a.scale_log2;
+  float m = -INFINITY, l = 0.f, o[kO];
+#pragma unroll
+  for (int i = 0; i < kO; ++i) o[i] = 0.f;
+  for (int j0 = it.c0; j0 < end; j0 += 64) {
+    float z = -INFINITY;
+    if (j0 + lane < end) {
+      const elem *k = kc + element_at<T, D>(a, it, j0 + lane);
+      float dot = 0.f;
+#pragma unroll 1
+      for (int d = 0; d < D; d += 8) {
+        float x[8], y[8];
+        load8<T>(q + d, x);
+        load8<T>(k + d, y);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) dot = fmaf(x[e], y[e], dot);
+      }
+      z = dot * scale;
+    }
+    float mn = fmaxf(m, z);
+    for (int s = 32; s > 0; s >>= 1) mn = fmaxf(mn, __shfl_xor(mn, s));
+    const float c = m == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(m - mn);
+    const float e = __builtin_amdgcn_exp2f(z - (mn == -INFINITY ? 0.f : mn));
+    float sum = e;
+    for (int s = 32; s > 0; s >>= 1) sum += __shfl_xor(sum, s);
+    m = mn;
+    l = l * c + sum;
+#pragma unroll
+    for (int i = 0; i < kO; ++i) o[i] *= c;
+    const int n = end - j0 < 64 ? end - j0 : 64;
+#pragma unroll 1
+    for (int i = 0; i < n; ++i) {
+      const float w = __shfl(e, i);
+      const int j = j0 + i;
+      const elem *v = vc + element_at<T, D>(a, it, j & ~7) + (j & 7);
+#pragma unroll
+      for (int u = 0; u < kO; ++u)
+        if (lane + 64 * u < D) o[u] += w * (float)v[8 * (lane + 64 * u)];
+    }
+  }
+  const bool direct = a.prefix_parts + a.suffix_parts == 1;
+  const int64_t at = it.part * (a.tokens * a.n_q_heads) + flat;
+  const float inv = l == 0.f ? 0.f : 1.0f / l;
+#pragma unroll
+  for (int u = 0; u < kO; ++u) {
+    const int d = lane + 64 * u;
+    if (d >= D) continue;
+    if (direct) static_cast<elem *>(a.out)[flat * D + d] = (elem)(o[u] * inv);
+    else a.part_o[at * D + d] = o[u];
+  }
+  if (lane) return;
+  if (!direct) a.part_ml[at] = make_float2(m, l);
+  else if (a.lse) a.lse[flat] = l == 0.f ? -INFINITY : (m + __log2f(l)) * 0.6931471805599453f;
+}
+
 // ---- few rows -------------------------------------------------------------------
 template <int D, int NW>
 struct Rows16 {
@@ -266,6 +371,19 @@ __device__ __forceinline__ void rows16_body(const AttnPrefix &a, const Item &it,
 #pragma unroll
       for (int r = 0; r < 4; ++r) o[i][r] *= c;
       o[i] = T::mfma16(vf[i], p, o[i]);
+    }
+  }
+
+  if (it.c1 > all_see) {
+    bool bad = false;
+#pragma unroll
+    for (int i = 0; i < kDT; ++i)
+#pragma unroll
+      for (int r = 0; r < 4; ++r) bad = bad || o[i][r] != o[i][r];
+    if (__syncthreads_or(live && bad) && edge_not_finite<T, D>(a, it, all_see)) {
+      const int end = it.row0 + kRows < it.rows ? it.row0 + kRows : it.rows;
+      for (int i = it.row0 + wave; i < end; i += NW) row_alone<T, D>(a, it, i);
+      return;
     }
   }
 
@@ -687,6 +805,21 @@ __device__ __forceinline__ void wide_body(const AttnPrefix &a, const Item &it, u
 #pragma unroll
         for (int w = 0; w < R; ++w) s[w] = s2[w];
       }
+    }
+  }
+
+  if (it.c1 > all_see) {
+    bool bad = false;
+#pragma unroll
+    for (int w = 0; w < R; ++w)
+#pragma unroll
+      for (int i = 0; i < kDT; ++i)
+#pragma unroll
+        for (int r = 0; r < 16; ++r) bad = bad || (live[w] && o[w][i][r] != o[w][i][r]);
+    if (__any(bad) && edge_not_finite<T, D>(a, it, all_see)) {
+      const int end = row0 + 32 * R < it.rows ? row0 + 32 * R : it.rows;
+      for (int i = row0; i < end; ++i) row_alone<T, D>(a, it, i);
+      return;
     }
   }
 

@@ -216,6 +216,37 @@ def test_attention_many_rows_share_a_prefix(batch, hq, hkv, d, prefix, t):
     check_attn(lens, [1] * batch, hq, hkv, d, 16, prefix, t, seed=batch)
 
 
+@pytest.mark.parametrize("value", ["nan", "inf"])
+@pytest.mark.parametrize("lens, news, hq, hkv, d, t", [
+    ([9], [7], 2, 1, 64, "f16"), ([140, 40], [9, 3], 4, 2, 128, "bf16"), ([90], [70], 2, 2, 96, "f16"),
+    ([300, 64], [290, 64], 2, 2, 64, "bf16"), ([300, 64], [290, 64], 2, 1, 128, "f16"),
+    ([200], [100], 2, 1, 256, "bf16"),
+])
+@pytest.mark.parametrize("prefix", [0, 50])
+def test_attention_later_tokens_are_not_seen(lens, news, hq, hkv, d, t, prefix, value):
+    """A value vector that is not finite reaches only the rows that see its key:
+    not the new tokens before it, whose mask leaves it out."""
+    q, kc, vc, table, ln, pids, start = make_attn(lens, news, hq, hkv, d, 16, prefix, t, 5)
+    announce(f"attn {value} behind the mask lens={lens} new={news} h={hq}/{hkv} d={d} prefix={prefix} {t}")
+    wo, _, bo, _ = so.attention(np64(q), np64(kc), np64(vc), table, list(lens), pids, prefix, start,
+                                d ** -0.5, t)
+    clear = np.zeros(len(q), dtype=bool)  # rows that see no such value
+    for b, (n, new) in enumerate(zip(lens, news)):
+        at = n - 1 - new // 3
+        kc[table[b, at // 16], :, at % 16] = float(value)
+        vc[table[b, at // 16], :, at % 16 // 8, :, at % 8] = float(value)
+        clear[start[b]:start[b] + at - (n - new)] = True
+    up = lambda a: torch.from_numpy(np.ascontiguousarray(a)).to(DEV)  # noqa: E731
+    out = bq.lqmm_attn_prefix(q.to(DEV), kc.to(DEV), vc.to(DEV), up(table), up(ln),
+                              prefix_pages=up(pids) if prefix else None, prefix_len=prefix,
+                              q_start=up(start), max_q=max(news))
+    assert clear.any() and not clear.all()
+    got = np64(out)
+    within(got[clear], wo[clear], bo[clear], "out")
+    if value == "nan":
+        assert np.isnan(got[~clear]).all()
+
+
 def test_attention_large_logits_and_ties():
     """A scale that makes one weight of each row nearly 1, and a scale of zero
     (all seen keys weigh the same)."""
