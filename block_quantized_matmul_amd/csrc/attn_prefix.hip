@@ -126,9 +126,8 @@ __device__ __forceinline__ uint32_t spread(uint32_t block, uint32_t n) {
 // new token with such a value would reach the new tokens before it, whose mask
 // leaves it out, through the matrix products. That leaves NaN in O, which is
 // looked for once, behind the keys' loop; rows of a block that has such a
-// value among the keys of its mask's edge are done again, by themselves. (The
-// test at the end costs nothing that can be measured; the values' own test in
-// the loop would be done for every key of the edge.)
+// value among the keys of its mask's edge are done again, by themselves.
+// (A test of the values in the loop would be made for every key of the edge.)
 template <class T, int D>
 __device__ __forceinline__ int64_t element_at(const AttnPrefix &a, const Item &it, int j) {
   const int32_t p = it.pages[j >> a.page_log2];
@@ -488,8 +487,30 @@ struct Wide {
   static constexpr int kLds = (kStagesK + kStagesV) * kHalf;
 };
 
+// The rows of a wave again, if its mask's edge asks for it (whether it did). Item
+// and arguments are read once more, so that nothing of them is held in registers
+// through the keys' loop for this (768 rows x 32801 keys of 128: 159 us with the
+// loop's own, 154 so; the 16-row kernel has registers to spare and is slower this
+// way, 24 x 4111 keys 154 / 161 us).
+template <class T, int D>
+__device__ __forceinline__ bool wave_again(uint32_t item0, int rows_per_block, int from, int n) {
+  uint64_t args = (uint64_t)__builtin_amdgcn_kernarg_segment_ptr();
+  uint32_t block = blockIdx.x;
+  asm volatile("" : "+s"(args), "+s"(block));
+  const AttnPrefix &a = *reinterpret_cast<const AttnPrefix *>(args);  // the kernel's first argument
+  Item it;
+  if (!find_item(a, item0 + spread(block, gridDim.x), rows_per_block, it)) return false;
+  const int row0 = it.row0 + from;
+  if (row0 >= it.rows || !edge_not_finite<T, D>(a, it, it.past + it.per_token * (row0 / a.group)))
+    return false;
+  const int end = row0 + n < it.rows ? row0 + n : it.rows;
+  for (int i = row0; i < end; ++i) row_alone<T, D>(a, it, i);
+  return true;
+}
+
 template <class T, int D, int NW, int R>
-__device__ __forceinline__ void wide_body(const AttnPrefix &a, const Item &it, uint8_t *smem) {
+__device__ __forceinline__ void wide_body(const AttnPrefix &a, const Item &it, uint32_t item0,
+                                          uint8_t *smem) {
   typedef typename T::elem elem;
   typedef typename T::vec8 vec8;
   typedef Wide<D> C;
@@ -808,19 +829,15 @@ __device__ __forceinline__ void wide_body(const AttnPrefix &a, const Item &it, u
     }
   }
 
-  if (it.c1 > all_see) {
-    bool bad = false;
+  if (it.c1 > plain_end) {
+    bool bad = false;  // (of rows that are there)
 #pragma unroll
     for (int w = 0; w < R; ++w)
 #pragma unroll
       for (int i = 0; i < kDT; ++i)
 #pragma unroll
         for (int r = 0; r < 16; ++r) bad = bad || (live[w] && o[w][i][r] != o[w][i][r]);
-    if (__any(bad) && edge_not_finite<T, D>(a, it, all_see)) {
-      const int end = row0 + 32 * R < it.rows ? row0 + 32 * R : it.rows;
-      for (int i = row0; i < end; ++i) row_alone<T, D>(a, it, i);
-      return;
-    }
+    if (__any(bad) && wave_again<T, D>(item0, 32 * R * NW, 32 * R * wave, 32 * R)) return;
   }
 
   const int64_t nrows = a.tokens * a.n_q_heads;
@@ -860,7 +877,7 @@ attn_wide_kernel(AttnPrefix a, uint32_t item0) {
   extern __shared__ __attribute__((aligned(16))) uint8_t smem[];
   Item it;
   if (find_item(a, item0 + spread(blockIdx.x, gridDim.x), 32 * R * NW, it))
-    wide_body<T, D, NW, R>(a, it, smem);
+    wide_body<T, D, NW, R>(a, it, item0, smem);
 }
 
 // Joins the partial results of each row: D / 4 threads a row, four
