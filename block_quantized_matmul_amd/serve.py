@@ -86,16 +86,24 @@ class SharedPromptAttention:
 
     def step(self, x):
         """One new token of every conversation, x (batch, hidden): the block's
-        output. The conversations' lengths advance by one."""
+        output. The conversations' lengths advance by one. A conversation that
+        already fills its max_pages pages gets no token and keeps its length;
+        its row of the output is NaN (lengths are known on the device only, so
+        that neither an eager step nor a replayed one can raise)."""
+        torch = self.torch
         q, k, v = self._project(x)
-        n = self.lens.long()
-        slots = self.pages[self.rows, n // self.ps].long() * self.ps + n % self.ps
+        most = self.pages.shape[1] * self.ps
+        n = self.lens.clamp(0, most).long()
+        full = n == most
+        at = (n // self.ps).clamp_(max=self.pages.shape[1] - 1)
+        slots = torch.add(n % self.ps, self.pages[self.rows, at], alpha=self.ps)
+        slots.masked_fill_(full, -1)  # not appended
         q = self.bq.lqmm_kv_append(q, k, v, self.lens + self.prompt_len, slots, self.k_cache,
                                    self.v_cache, self.turns)
-        self.lens += 1
+        torch.add(n, ~full, out=self.lens)
         o = self.bq.lqmm_attn_prefix(q, self.k_cache, self.v_cache, self.pages, self.lens,
                                      prefix_pages=self.prompt_pages, prefix_len=self.prompt_len)
-        return self._output(o)
+        return self._output(o).masked_fill_(full[:, None], float("nan"))
 
     def capture(self, x):
         """A HIP graph of one step that reads x; returns (graph, output). Steps
