@@ -19,6 +19,10 @@
 // exponentials of the two tiles are, in place, the B operand of the second
 // product, and no value crosses a lane except the row maximum.
 //
+// A row or part that sees no key has the sum 0. Its maximum, -infinity, does not
+// tell: maxima leave NaN out, so that a row whose every logit is NaN has it too,
+// with a sum of NaN, which has to reach the output.
+//
 // P is rounded to the cache's 16-bit type, as the matrix cores want it; in
 // fp16 it is kept at 2^kShift times its value, so that weights down to
 // 2^-(24 + kShift) of the largest do not vanish. Logits, maxima, sums and O
@@ -405,8 +409,8 @@ __device__ __forceinline__ void rows16_body(const AttnPrefix &a, const Item &it,
   for (int w = 0; w < NW; ++w) mo = fmaxf(mo, sm.wave_m[w][out_row]);
 #pragma unroll
   for (int w = 0; w < NW; ++w) {
-    const float mw = sm.wave_m[w][out_row];
-    lj += mw == -INFINITY ? 0.f : sm.wave_l[w][out_row] * __builtin_amdgcn_exp2f(mw - mo);
+    const float mw = sm.wave_m[w][out_row], lw = sm.wave_l[w][out_row];
+    lj += lw == 0.f ? 0.f : lw * __builtin_amdgcn_exp2f(mw - mo);
   }
   const int orow = it.row0 + out_row;
   const bool owrite = orow < it.rows;
@@ -900,10 +904,10 @@ attn_join_kernel(AttnPrefix a) {
   float4_t o = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll 4
   for (int p = 0; p < parts; ++p) {
-    // a part that sees no key has m = -inf: nothing of it counts
+    // of a part that sees no key nothing counts
     const float2 ml = a.part_ml[p * nrows + row];
     const float4_t x = *reinterpret_cast<const float4_t *>(a.part_o + (p * nrows + row) * D + d);
-    const bool seen = ml.x != -INFINITY;
+    const bool seen = ml.y != 0.f;
     const float w = seen ? __builtin_amdgcn_exp2f(ml.x - m) : 0.f;
     l += w * (seen ? ml.y : 0.f);
 #pragma unroll

@@ -1,0 +1,133 @@
+"""Edges of the serving operators: what NaN, infinite and very large values, rows
+of no sequence and products that cancel must come to, against the 64-bit forms
+and the bounds of serve_oracle.py."""
+import numpy as np
+import pytest
+
+import block_quantized_matmul_amd as bq
+import serve_oracle as so
+from gpu_util import announce
+from test_serve_gpu import DEV, DT, f8_dev, make_attn, np64, within
+
+pytestmark = pytest.mark.gpu
+
+torch = pytest.importorskip("torch")
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _gpu():
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+    bq.load()
+
+
+# ---- NaN logits ------------------------------------------------------------------
+# Sizes that take every way through the kernels: the 16-row and the wide kernel,
+# one part (written directly) and several (joined).
+SHAPES = [
+    # lens, new tokens, heads, dimensions, prefix, type
+    ([97], [1], 2, 1, 64, 0, "f16"), ([70, 3], [1, 1], 4, 2, 128, 70, "bf16"),
+    ([2700], [1], 2, 1, 64, 0, "f16"), ([41, 33], [3, 2], 4, 2, 256, 0, "bf16"),
+    ([90], [70], 2, 2, 96, 0, "f16"), ([150, 64], [140, 64], 2, 1, 128, 0, "bf16"),
+    ([100, 64], [90, 64], 2, 2, 64, 50, "bf16"), ([80], [60], 2, 1, 256, 50, "f16"),
+    ([int(n) for n in range(35)], [1] * 35, 4, 1, 128, 130, "f16"),
+]
+
+
+class Batch:
+    """One batch on the host, run through the library and the 64-bit form."""
+
+    def __init__(self, lens, news, hq, hkv, d, prefix, t, what):
+        announce(f"attn {what} lens={lens[:4]} new={news[:4]} h={hq}/{hkv} d={d} prefix={prefix} {t}")
+        self.lens, self.news, self.prefix, self.t, self.d = lens, news, prefix, t, d
+        (self.q, self.kc, self.vc, self.table, self.ln, self.pids,
+         self.start) = make_attn(lens, news, hq, hkv, d, 16, prefix, t, sum(lens) + d)
+
+    def want(self):
+        return so.attention(np64(self.q), np64(self.kc), np64(self.vc), self.table, self.lens, self.pids,
+                            self.prefix, self.start, self.d ** -0.5, self.t)
+
+    def run(self, **kw):
+        up = lambda a: torch.from_numpy(np.ascontiguousarray(a)).to(DEV)  # noqa: E731
+        if any(n != 1 for n in self.news):
+            kw = dict(q_start=up(self.start), max_q=max(self.news)) | kw
+        out, lse = bq.lqmm_attn_prefix(self.q.to(DEV), self.kc.to(DEV), self.vc.to(DEV), up(self.table),
+                                       up(self.ln), prefix_pages=up(self.pids) if self.prefix else None,
+                                       prefix_len=self.prefix, return_lse=True, **kw)
+        return np64(out), np64(lse)
+
+    def keys_of(self, b, j0, j1):
+        """(page, place) of sequence b's keys j0 .. j1 - 1."""
+        return [(self.table[b, j // 16], j % 16) for j in range(j0, min(j1, self.lens[b]))]
+
+    def first_seen(self, b, j):
+        """The first row of sequence b that sees its key j."""
+        return self.start[b] + max(0, j - (self.lens[b] - self.news[b]))
+
+
+def compare(out, lse, want, nan):
+    """Rows in `nan` (tokens, or tokens x heads) are NaN, out and lse; the others
+    within their bounds."""
+    wo, wl, bo, bl = want
+    nan = np.broadcast_to(nan if nan.ndim == 2 else nan[:, None], wl.shape)
+    assert np.isnan(out[nan]).all() and np.isnan(lse[nan]).all()
+    within(out[~nan], wo[~nan], bo[~nan], "out")
+    empty = np.isneginf(wl) & ~nan
+    assert np.array_equal(np.isneginf(lse), empty)
+    some = ~nan & ~empty
+    within(lse[some], wl[some], bl[some], "lse")
+
+
+@pytest.mark.parametrize("case", SHAPES)
+def test_a_nan_query_gives_nan(case):
+    """A row whose every logit is NaN is not a row that sees no key, however its
+    keys are split."""
+    b = Batch(*case, "NaN queries")
+    want = b.want()
+    nan = np.zeros(b.q.shape[:2], dtype=bool)
+    nan[-1, 0] = nan[len(nan) // 2, -1] = True
+    b.q[torch.from_numpy(nan)] = float("nan")
+    sees = np.isfinite(want[1])  # a row without keys has no logit
+    compare(*b.run(), want, nan & sees)
+
+
+@pytest.mark.parametrize("part", ["sequence", "a wave's keys", "prefix"])
+@pytest.mark.parametrize("case", SHAPES)
+def test_keys_that_are_all_nan_give_nan(case, part):
+    """A part, or the keys that one wave takes, whose logits are all NaN."""
+    b = Batch(*case, f"NaN keys: {part}")
+    want = b.want()
+    nan = np.zeros(len(b.q), dtype=bool)
+    if part == "prefix":
+        if not b.prefix:
+            pytest.skip("no prefix")
+        b.kc[b.pids.astype(np.int64)] = float("nan")
+        nan[:] = True
+    else:
+        last = len(b.lens) - 1
+        j0, j1 = (0, b.lens[last]) if part == "sequence" else (32, 64)
+        if j0 >= b.lens[last]:
+            j0, j1 = 0, 32
+        for page, place in b.keys_of(last, j0, j1):
+            b.kc[page, :, place] = float("nan")
+        nan[b.first_seen(last, j0):b.start[last + 1]] = True
+    compare(*b.run(), want, nan)
+
+
+@pytest.mark.parametrize("case", [c for c in SHAPES if max(c[1]) > 1])
+def test_a_nan_query_among_rows_done_again(case):
+    """The rows of a mask's edge that are computed by themselves, because a value
+    behind it is infinite, keep the NaN of their queries."""
+    b = Batch(*case, "NaN query beside an infinite value")
+    want = b.want()
+    n, new = b.lens[0], b.news[0]
+    page, place = b.keys_of(0, n - 1, n)[0]
+    b.vc[page, :, place // 8, :, place % 8] = float("inf")
+    seen = np.zeros(len(b.q), dtype=bool)
+    seen[b.start[1] - 1] = True  # the only row that sees the infinite value
+    nan = np.zeros(b.q.shape[:2], dtype=bool)
+    nan[b.start[1] - 2, 0] = True
+    b.q[torch.from_numpy(nan)] = float("nan")
+    out, lse = b.run()
+    keep = ~seen
+    compare(out[keep], lse[keep], [w[keep] for w in want], nan[keep])
