@@ -406,29 +406,22 @@ def _calls():
                 f"_serve.so not found at {path}; build it with "
                 "`python -m block_quantized_matmul_amd.build` (there is no fallback path)")
         from . import _serve as module  # (the compiled module)
-        module.setup(_check, torch._C._cuda_getCurrentRawStream, _scratch_for)
+        module.setup(_check, torch._C._cuda_getCurrentRawStream, _workspace_on)
         _native = module
     return _native
 
 
-# Scratch for attention's partial results when the caller passes no workspace:
-# one buffer per (device, stream), at least doubled when it grows. A buffer
-# that was outgrown is kept (they add up to less than the newest): launches in
-# flight and captured graphs may still use it.
-_scratch = {}
-
-
-def _scratch_for(index, stream_handle, nbytes):
+# Workspace for a call that was given another stream than the current one: the
+# allocator's memory of that stream, so that it is handed out again in that
+# stream's order (a graph that is being captured there gets its own). On the
+# current stream the native call allocates it by itself.
+def _workspace_on(index, stream, nbytes):
     torch = _torch()
-    bufs = _scratch.setdefault((index, stream_handle), [])
-    if not bufs or bufs[-1].numel() < nbytes:
-        grown = max(nbytes, 2 * bufs[-1].numel() if bufs else 1 << 20)
-        bufs.append(torch.empty(grown, dtype=torch.uint8, device=torch.device("cuda", index)))
-        # The memory may have been freed on the current stream a moment ago:
-        # nothing may still use it when another stream's launch writes it.
-        if not torch.cuda.is_current_stream_capturing():
-            torch.cuda.synchronize(index)
-    return bufs[-1]
+    if isinstance(stream, int):
+        stream = (torch.cuda.ExternalStream(stream, device=index) if stream
+                  else torch.cuda.default_stream(index))
+    with torch.cuda.stream(stream):
+        return torch.empty(nbytes, dtype=torch.uint8, device=torch.device("cuda", index))
 
 
 def kv_cache_empty(num_pages, n_kv_heads, page_size, head_dim, dtype=None, device="cuda"):
@@ -483,7 +476,9 @@ def lqmm_attn_prefix(q, k_cache, v_cache, pages, seq_lens, prefix_pages=None, pr
     rows q_start[b] .. q_start[b + 1] - 1 (int32, batch + 1 entries) with at
     most ``max_q`` of them. scale: 1 / sqrt(head_dim) when None. Returns out
     (tokens, n_q_heads, head_dim), or (out, lse) with lse (tokens, n_q_heads)
-    float32 when return_lse is set or lse is given."""
+    float32 when return_lse is set or lse is given. workspace: a uint8 device
+    tensor of lqmm_attn_prefix_workspace_bytes that no call which may overlap
+    uses; None allocates one for the call, in the memory of its stream."""
     return _calls().attn_prefix(q, k_cache, v_cache, pages, seq_lens, prefix_pages, prefix_len,
                                 q_start, max_q, scale, out, return_lse, lse, workspace, stream)
 

@@ -23,7 +23,7 @@ namespace {
 
 PyObject *g_raise_status = nullptr;  // raises the package's error for a status
 PyObject *g_raw_stream = nullptr;    // current stream's handle of a device index
-PyObject *g_scratch = nullptr;       // scratch tensor for (index, stream, bytes)
+PyObject *g_workspace_on = nullptr;  // workspace for (device index, stream, bytes)
 
 struct Failed {};  // a Python error is set
 
@@ -316,6 +316,7 @@ PyObject *attn_prefix(PyObject *, PyObject *const *a, Py_ssize_t n) {
     void *stream = stream_of(a[14], q);
     void *ws = nullptr;
     size_t ws_bytes = 0;
+    at::Tensor scratch;
     if (a[13] != Py_None) {
       const at::Tensor &w = whole(a[13], at::kByte, "workspace");
       same_device(q, w);
@@ -324,15 +325,21 @@ PyObject *attn_prefix(PyObject *, PyObject *const *a, Py_ssize_t n) {
     } else {
       const size_t need = lqmm_attn_prefix_workspace_bytes(prefix_len, max_pages, max_q, tokens, batch,
                                                            heads, c.heads, c.dim, c.page_size);
-      if (need) {
-        PyObject *w = PyObject_CallFunction(g_scratch, "iKK", (int)q.get_device(),
-                                            (unsigned long long)(uintptr_t)stream,
+      // Its own workspace for every call, from the allocator's memory of the
+      // stream it runs on: freed behind the launches, it is handed out again in
+      // stream order, to whatever thread, and a graph under capture has its own.
+      if (need && (a[14] == Py_None || stream == stream_of(Py_None, q))) {
+        scratch = at::empty({(int64_t)need}, q.options().dtype(at::kByte));
+      } else if (need) {
+        PyObject *w = PyObject_CallFunction(g_workspace_on, "iOK", (int)q.get_device(), a[14],
                                             (unsigned long long)need);
         if (!w) throw Failed();
-        // (the package keeps the buffer)
-        ws = THPVariable_Unpack(w).data_ptr();
-        ws_bytes = (size_t)THPVariable_Unpack(w).numel();
+        scratch = THPVariable_Unpack(w);
         Py_DECREF(w);
+      }
+      if (need) {
+        ws = scratch.data_ptr();
+        ws_bytes = (size_t)scratch.numel();
       }
     }
     float *lse_p = lse.defined() ? static_cast<float *>(lse.data_ptr()) : nullptr;
@@ -445,7 +452,7 @@ PyObject *gemm_f8b128(PyObject *, PyObject *const *a, Py_ssize_t n) {
 
 PyObject *setup(PyObject *, PyObject *const *a, Py_ssize_t n) {
   if (!arity(n, 3)) return nullptr;
-  PyObject **to[] = {&g_raise_status, &g_raw_stream, &g_scratch};
+  PyObject **to[] = {&g_raise_status, &g_raw_stream, &g_workspace_on};
   for (int i = 0; i < 3; ++i) {
     Py_INCREF(a[i]);
     Py_XDECREF(*to[i]);
@@ -456,7 +463,7 @@ PyObject *setup(PyObject *, PyObject *const *a, Py_ssize_t n) {
 
 #define FASTCALL(f) reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(f)), METH_FASTCALL
 PyMethodDef kMethods[] = {
-    {"setup", FASTCALL(setup), "setup(raise_status, raw_stream, scratch)"},
+    {"setup", FASTCALL(setup), "setup(raise_status, raw_stream, workspace_on)"},
     {"kv_append", FASTCALL(kv_append), nullptr},
     {"attn_prefix", FASTCALL(attn_prefix), nullptr},
     {"quant_f8b128", FASTCALL(quant_f8b128), nullptr},

@@ -111,7 +111,7 @@ class SharedPromptAttention:
         torch = self.torch
         side = torch.cuda.Stream()
         side.wait_stream(torch.cuda.current_stream())
-        with torch.cuda.stream(side):  # the first step makes this stream's scratch
+        with torch.cuda.stream(side):  # a first step outside the graph loads the kernels
             kept = self.lens.clone()
             self.step(x)
             self.lens.copy_(kept)

@@ -85,3 +85,30 @@ def test_lengths_out_of_range_reach_no_page(monkeypatch, bad):
     slots = calls.slots[-1]
     assert slots[0] == 8 and slots[2] == 40 and (slots[1] == -1 or 24 <= slots[1] < 40)
     assert 0 <= calls.lens[-1][1] <= 16
+
+
+def test_workspaces_are_allocated_for_each_call_on_its_stream(monkeypatch):
+    """What a call on another stream than the current one works in is new, and
+    that stream's: nothing is kept and handed to another call."""
+    import contextlib
+    from types import SimpleNamespace
+
+    import block_quantized_matmul_amd as bq
+    on = [None]
+
+    @contextlib.contextmanager
+    def stream(s):
+        on.append(s)
+        yield
+        on.pop()
+
+    cuda = SimpleNamespace(stream=stream, default_stream=lambda i: ("default", i),
+                           ExternalStream=lambda h, device: ("external", h, device))
+    fake = SimpleNamespace(cuda=cuda, uint8="u8", device=lambda *a: a,
+                           empty=lambda n, dtype, device: [n, dtype, device, on[-1]])
+    monkeypatch.setattr(bq, "_torch", lambda: fake)
+    held = SimpleNamespace(cuda_stream=9)
+    a, b = bq._workspace_on(1, held, 64), bq._workspace_on(1, held, 64)
+    assert a is not b and a == [64, "u8", ("cuda", 1), held]
+    assert bq._workspace_on(0, 77, 8)[3] == ("external", 77, 0)
+    assert bq._workspace_on(0, 0, 8)[3] == ("default", 0) and on == [None]

@@ -66,3 +66,82 @@ def test_full_conversations_write_nothing(at, replayed):
     others = [p for p in range(len(k)) if p not in mine.tolist()]
     assert torch.equal(full.k_cache[others], free.k_cache[others])
     assert torch.equal(full.v_cache[others], free.v_cache[others])
+
+
+# ---- workspaces that the caller does not pass ------------------------------------
+def split_call(seed, batch=24, prefix=700):
+    """Arguments of an attention call whose keys are split, and its output by itself."""
+    g = torch.Generator(device="cuda")
+    g.manual_seed(seed)
+    r = lambda *s: torch.randn(*s, device="cuda", generator=g).half()  # noqa: E731
+    pp, hkv, d, ps = -(-prefix // 16), 2, 128, 16
+    i32 = dict(dtype=torch.int32, device="cuda")
+    args = (r(batch, 8, d), r(pp + 4 * batch, hkv, ps, d), r(pp + 4 * batch, hkv, ps // 8, d, 8),
+            pp + torch.arange(4 * batch, **i32).view(batch, 4), torch.arange(batch, **i32) % 60 + 1)
+    kw = dict(prefix_pages=torch.arange(pp, **i32), prefix_len=prefix)
+    assert bq.lqmm_attn_prefix_workspace_bytes(prefix, 4, 1, batch, batch, 8, hkv, d, ps) > 0
+    out = bq.lqmm_attn_prefix(*args, **kw)
+    torch.cuda.synchronize()
+    return args, kw, out
+
+
+@pytest.mark.parametrize("where", ["current", "stream", "handle", "default"])
+def test_a_call_keeps_no_workspace(where):
+    announce(f"attn workspace of a call on {where}")
+    args, kw, want = split_call(1)
+    out, s = torch.empty_like(want), torch.cuda.Stream()
+    torch.cuda.synchronize()
+    before = torch.cuda.memory_allocated()
+    for _ in range(3):
+        if where == "default":  # (the stream's handle is 0)
+            with torch.cuda.stream(s):
+                bq.lqmm_attn_prefix(*args, **kw, out=out, stream=0)
+        else:
+            bq.lqmm_attn_prefix(*args, **kw, out=out, stream={"current": None, "stream": s, "handle": s.cuda_stream}[where])
+        torch.cuda.synchronize()
+        assert torch.equal(out, want)
+    assert torch.cuda.memory_allocated() == before
+
+
+def test_graphs_of_one_capture_stream_run_beside_each_other():
+    """Two graphs captured on one stream, replayed on two, beside eager calls on
+    the capture stream: each gives what it gives alone."""
+    s, calls = torch.cuda.Stream(), [split_call(seed) for seed in (1, 2, 3)]
+    graphs = []
+    for args, kw, _ in calls[:2]:
+        announce("attn graphs of one capture stream")
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=s):
+            outs = [bq.lqmm_attn_prefix(*args, **kw) for _ in range(8)]
+        graphs.append((graph, outs))
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    for i in range(10):
+        torch.cuda.synchronize()
+        for (graph, outs), on in zip(graphs, streams):
+            with torch.cuda.stream(on):
+                for o in outs:
+                    o.zero_()
+                graph.replay()
+        with torch.cuda.stream(s):
+            eager = [bq.lqmm_attn_prefix(*calls[2][0], **calls[2][1]) for _ in range(8)]
+        torch.cuda.synchronize()
+        assert all(torch.equal(o, calls[2][2]) for o in eager)
+        for (_, outs), (_, _, want) in zip(graphs, calls):
+            assert all(torch.equal(o, want) for o in outs), i
+
+
+def test_threads_of_one_stream_do_not_share_a_workspace():
+    import threading
+    calls, wrong = [split_call(seed) for seed in (4, 5, 6)], []
+
+    def work(args, kw, want):
+        outs = [bq.lqmm_attn_prefix(*args, **kw) for _ in range(200)]
+        wrong.append(sum(not torch.equal(o, want) for o in outs))
+
+    announce("attn from three threads on one stream")
+    threads = [threading.Thread(target=work, args=c) for c in calls]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert wrong == [0, 0, 0]
