@@ -96,15 +96,16 @@ __device__ __forceinline__ bool find_item(const AttnPrefix &a, uint32_t idx, int
     q1 = a.q_start[b + 1];
     q0 = q0 < 0 ? 0 : q0 < a.tokens ? q0 : a.tokens;
     q1 = q1 < q0 ? q0 : q1 < a.tokens ? q1 : a.tokens;
-    if (q1 - q0 > a.max_q) q1 = q0 + a.max_q;
   }
-  const int n = (int)(q1 - q0);
+  // (rows past max_q are left out, and still are new tokens of the sequence)
+  const int news = (int)(q1 - q0);
+  const int n = a.max_q < news ? (int)a.max_q : news;
   it.part = a.prefix_parts + chunk;
   it.tok0 = q0;
   it.rows = n * G;
   it.row0 = rb * rows_per_block;
   if (it.row0 >= it.rows) return false;
-  it.past = (int)len - n + 1;
+  it.past = (int)len - news + 1;
   it.per_token = 1;
   it.pages = a.pages + b * a.max_pages;
   const int64_t c0 = (int64_t)chunk * a.suffix_chunk;

@@ -131,3 +131,19 @@ def test_a_nan_query_among_rows_done_again(case):
     out, lse = b.run()
     keep = ~seen
     compare(out[keep], lse[keep], [w[keep] for w in want], nan[keep])
+
+
+# ---- more new tokens than max_q --------------------------------------------------
+@pytest.mark.parametrize("lens, news, max_q, hq, hkv, d, prefix, t", [
+    ([50, 30], [9, 4], 5, 4, 2, 64, 0, "f16"), ([50, 30], [9, 4], 5, 4, 2, 256, 40, "bf16"),
+    ([120, 60], [100, 50], 77, 2, 2, 96, 60, "f16"), ([120], [100], 60, 4, 1, 128, 0, "bf16"),
+    ([5, 40], [9, 3], 6, 2, 1, 64, 0, "f16"),
+])
+def test_rows_below_max_q_keep_their_masks(lens, news, max_q, hq, hkv, d, prefix, t):
+    """Leaving out a sequence's rows past max_q changes nothing of the others:
+    token i of n still sees the keys 0 .. len - n + i."""
+    b = Batch(lens, news, hq, hkv, d, prefix, t, f"max_q {max_q}")
+    want = b.want()
+    rows = np.concatenate([np.arange(s, s + min(n, max_q)) for s, n in zip(b.start, news)])
+    out, lse = b.run(max_q=max_q)
+    compare(out[rows], lse[rows], [w[rows] for w in want], np.zeros(len(rows), dtype=bool))
