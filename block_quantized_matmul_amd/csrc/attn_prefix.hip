@@ -119,6 +119,47 @@ __device__ __forceinline__ bool find_item(const AttnPrefix &a, uint32_t idx, int
   return true;
 }
 
+// Rows of q that belong to no sequence (before q_start[0], past max_q of a
+// sequence's, from q_start[batch] on) see no key: out is 0 and lse -infinity.
+// The first workgroup of a sequence and key head does those beside its rows. Where
+// results are joined it leaves the sum kNoSequence in the first of the
+// sequences' parts, whose other entries for such rows nothing writes.
+constexpr float kNoSequence = -1.0f;
+
+template <class T, int D>
+__device__ __forceinline__ void rows_of_no_sequence(const AttnPrefix &a, uint32_t idx, int threads) {
+  if (!a.q_start || idx < (uint32_t)a.prefix_items) return;
+  idx -= (uint32_t)a.prefix_items;
+  const uint32_t first = (uint32_t)a.suffix_row_blocks * (uint32_t)a.suffix_parts;
+  if (idx % first) return;
+  idx /= first;
+  const int h = (int)(idx % (uint32_t)a.n_kv_heads), G = a.group;
+  const int64_t b = idx / (uint32_t)a.n_kv_heads;
+  int64_t q0 = a.q_start[b], q1 = a.q_start[b + 1];
+  q0 = q0 < 0 ? 0 : q0 < a.tokens ? q0 : a.tokens;
+  q1 = q1 < q0 ? q0 : q1 < a.tokens ? q1 : a.tokens;
+  if (q1 - q0 > a.max_q) q0 += a.max_q;
+  else q0 = q1;
+  if (b == a.batch - 1) q1 = a.tokens;
+  int64_t before = b == 0 ? a.q_start[0] : 0;  // tokens [0, before) and [q0, q1)
+  before = before < 0 ? 0 : before < a.tokens ? before : a.tokens;
+  const bool direct = a.prefix_parts + a.suffix_parts == 1;
+  constexpr int kVecs = D / 8;
+  const int per = direct ? G * kVecs : G;  // stores of a token
+  for (int64_t i = threadIdx.x; i < (before + q1 - q0) * per; i += threads) {
+    const int64_t n = i / per;
+    const int64_t t = n < before ? n : q0 + n - before;
+    const int in = (int)(i % per), g = direct ? in / kVecs : in;
+    const int64_t flat = t * a.n_q_heads + h * G + g;
+    if (!direct) {
+      a.part_ml[a.prefix_parts * (a.tokens * a.n_q_heads) + flat] = make_float2(-INFINITY, kNoSequence);
+      continue;
+    }
+    reinterpret_cast<u32x4 *>(static_cast<typename T::elem *>(a.out) + flat * D)[in % kVecs] = u32x4{0u, 0u, 0u, 0u};
+    if (a.lse && in % kVecs == 0) a.lse[flat] = -INFINITY;
+  }
+}
+
 // Workgroups are handed to the 8 XCDs in turn, and each has its own L2:
 // renumbered so that consecutive items, which share keys, run on one XCD.
 __device__ __forceinline__ uint32_t spread(uint32_t block, uint32_t n) {
@@ -466,7 +507,9 @@ __global__ void __launch_bounds__(kThreads)
 attn_rows16_kernel(AttnPrefix a, uint32_t item0) {
   __shared__ Rows16<D, kThreads / 64> sm;
   Item it;
-  if (find_item(a, item0 + spread(blockIdx.x, gridDim.x), kRows, it))
+  const uint32_t idx = item0 + spread(blockIdx.x, gridDim.x);
+  rows_of_no_sequence<T, D>(a, idx, kThreads);
+  if (find_item(a, idx, kRows, it))
     rows16_body<T, D, kThreads / 64>(a, it, sm);
 }
 
@@ -881,7 +924,9 @@ __global__ void __launch_bounds__(64 * NW, wide_waves(D, NW, R))
 attn_wide_kernel(AttnPrefix a, uint32_t item0) {
   extern __shared__ __attribute__((aligned(16))) uint8_t smem[];
   Item it;
-  if (find_item(a, item0 + spread(blockIdx.x, gridDim.x), 32 * R * NW, it))
+  const uint32_t idx = item0 + spread(blockIdx.x, gridDim.x);
+  rows_of_no_sequence<T, D>(a, idx, 64 * NW);
+  if (find_item(a, idx, 32 * R * NW, it))
     wide_body<T, D, NW, R>(a, it, item0, smem);
 }
 
@@ -913,6 +958,11 @@ attn_join_kernel(AttnPrefix a) {
     l += w * (seen ? ml.y : 0.f);
 #pragma unroll
     for (int r = 0; r < 4; ++r) o[r] += w * (seen ? x[r] : 0.f);
+  }
+  // of a row of no sequence nothing read above counts
+  if (a.q_start && a.part_ml[a.prefix_parts * nrows + row].y == kNoSequence) {
+    l = 0.f;
+    o = float4_t{0.f, 0.f, 0.f, 0.f};
   }
   const float inv = l == 0.f ? 0.f : 1.0f / l;
   elem *dst = static_cast<elem *>(a.out) + row * D + d;

@@ -308,11 +308,12 @@ lqmm_status lqmm_kv_append(const void *q, const void *k, const void *v, int in_t
  * query head h reads key head h / (n_q_heads / n_kv_heads). The tokens of
  * sequence b are rows q_start[b] .. q_start[b + 1] - 1 of q (int32, batch + 1
  * entries, on the device); NULL is one token per sequence (tokens == batch).
- * max_q is at least the largest count of them (1 with NULL q_start; rows past
- * it are left out). New token i of n sees the prefix and its sequence's keys
- * 0 .. seq_lens[b] - n + i. out: tokens x n_q_heads x head_dim of `type`; lse
+ * max_q is at least the largest count of them (1 with NULL q_start; a
+ * sequence's rows past it are left out). New token i of n sees the prefix and
+ * its sequence's keys 0 .. seq_lens[b] - n + i. out: tokens x n_q_heads x head_dim of `type`; lse
  * (NULL: not wanted): tokens x n_q_heads fp32, the logarithm of the sum of
- * exp(scale * q.k). A row that sees no key gets zeros and -infinity.
+ * exp(scale * q.k). A row that sees no key gets zeros and -infinity, and so does
+ * a row that is left out or lies outside q_start[0] .. q_start[batch] - 1.
  *
  * Logits, maxima, sums and outputs are fp32; the weights are rounded to `type`
  * for the second product and the output is rounded once. Lengths and page

@@ -147,3 +147,40 @@ def test_rows_below_max_q_keep_their_masks(lens, news, max_q, hq, hkv, d, prefix
     rows = np.concatenate([np.arange(s, s + min(n, max_q)) for s, n in zip(b.start, news)])
     out, lse = b.run(max_q=max_q)
     compare(out[rows], lse[rows], [w[rows] for w in want], np.zeros(len(rows), dtype=bool))
+
+
+# ---- rows of no sequence ---------------------------------------------------------
+@pytest.mark.parametrize("given", [True, False])
+@pytest.mark.parametrize("lens, news, max_q, before, after, hq, hkv, d, prefix, t", [
+    ([20, 9], [3, 2], 3, 0, 4, 2, 1, 64, 0, "f16"), ([20, 9], [3, 2], 3, 5, 4, 4, 2, 128, 40, "bf16"),
+    ([50, 30], [9, 4], 5, 2, 0, 4, 2, 64, 0, "f16"), ([50, 30], [9, 4], 5, 2, 300, 4, 2, 256, 40, "bf16"),
+    ([120, 60], [100, 50], 100, 3, 7, 2, 1, 128, 0, "f16"), ([120, 60], [100, 50], 77, 0, 40, 2, 2, 96, 60, "f16"),
+    ([2700], [2], 2, 1, 5, 2, 1, 64, 0, "bf16"), ([120], [100], 60, 40, 3, 4, 1, 64, 0, "bf16"),
+    ([0, 7], [0, 2], 2, 3, 3, 2, 1, 64, 30, "f16"),
+])
+def test_rows_of_no_sequence(lens, news, max_q, before, after, hq, hkv, d, prefix, t, given):
+    """Rows of q before q_start[0], from q_start[batch] on and past max_q of a
+    sequence's come out as rows without keys do, whatever the workspace and the
+    output held; nothing around them is written."""
+    b = Batch(lens, news, hq, hkv, d, prefix, t, "rows of no sequence")
+    wo, wl, bo, bl = b.want()
+    T = before + sum(news) + after
+    q = torch.full((T, hq, d), 3.0, dtype=DT[t])
+    q[before:before + sum(news)] = b.q
+    of = np.full(T, -1)  # the row of b.q that a row is
+    for s, n in zip(b.start, news):
+        of[before + s:before + s + min(n, max_q)] = np.arange(s, s + min(n, max_q))
+    b.q, b.start = q, b.start + np.int32(before)
+    args = dict(max_q=max_q, q_start=torch.from_numpy(b.start).to(DEV))
+    if given:
+        whole = torch.full((T + 2, hq, d), 7.0, dtype=DT[t], device=DEV)
+        lses = torch.full((T + 2, hq), 7.0, device=DEV)
+        need = bq.lqmm_attn_prefix_workspace_bytes(prefix, b.table.shape[1], max_q, T, len(lens), hq, hkv, d, 16)
+        ws = torch.full((need + 64,), 0xFF, dtype=torch.uint8, device=DEV)  # (NaN in fp32)
+        args |= dict(out=whole[1:-1], lse=lses[1:-1], workspace=ws[:need])
+    out, lse = b.run(**args)
+    if given:
+        assert (whole[[0, -1]] == 7).all() and (lses[[0, -1]] == 7).all() and (ws[need:] == 0xFF).all()
+    live = of >= 0
+    assert (out[~live] == 0).all() and np.isneginf(lse[~live]).all()
+    compare(out[live], lse[live], [w[of[live]] for w in (wo, wl, bo, bl)], np.zeros(live.sum(), dtype=bool))
