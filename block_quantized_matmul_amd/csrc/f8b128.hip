@@ -4,22 +4,23 @@
 // Mathematics. W is N x K codes with one scale for each 128 x 128 block, X is
 // M x K codes with one scale for each row and group of 128 columns:
 //   Y[m][n] = sum_b sx[b][m] sw[n / 128][b] sum_{k in block b} X[m][k] W[n][k].
-// One v_mfma_f32_16x16x128_f8f6f4 is the inner sum of one scale block for a
-// 16 x 16 tile, started from zero; the outer sum is one fp32 multiply-add
-// with the product of the two scales.
+// The inner sum of one scale block for a 16 x 16 tile is four
+// v_mfma_f32_16x16x32_f16, started from zero; the outer sum is one fp32
+// multiply-add with the product of the two scales.
 //
 // Which matrix cores. The f8 ones do not sum in fp32: a product is cut off
 // 14 bits below the largest of its group (measured: next to 448 * 448 =
-// 200704, products below 8 vanish and 9 counts as 8), a relative error of 1e-5
-// to 5e-5 of a sum. That is far below the rounding of a bf16 output (2^-8)
-// and not of the others, so bf16 products run on the f8 cores; for fp16 and
-// fp32 outputs the codes are turned into fp16 in registers (exactly) and
-// multiplied there, at half the rate, with fp32 sums.
+// 200704, products below 8 vanish and 9 counts as 8), so that behind two large
+// products that cancel a whole sum can be lost, whatever the output's type.
+// The codes are turned into fp16 in registers instead (exactly) and multiplied
+// there, at half the rate, with fp32 sums. What that costs with bf16 outputs
+// (us, f8 / fp16 cores): 1 x 28672 x 8192 36.2 / 35.9, 45 x 4127 x 4112 8.6 /
+// 11.8, 512 x 14336 x 4096 40 / 63, 4096 x 14336 x 4096 253 / 433.
 //
-// Layout. With W as the A operand, a lane holds
-// four outputs of one row m (m = lane & 15), so the scale product is one
-// value per lane and 16 rows of X: four multiply-adds per matrix
-// instruction, which run on the vector ALU beside it.
+// Layout. With W as the A operand, a lane holds four outputs of one row m
+// (m = lane & 15), so the scale product is one value per lane and 16 rows of X:
+// four multiply-adds per four matrix instructions, which run on the vector ALU
+// beside them.
 #include "lqmm_internal.hpp"
 #include "serve_device.hpp"
 
@@ -117,23 +118,11 @@ __device__ __forceinline__ void to_f16(i32x8 c, half8_t (&h)[4]) {
 }
 
 // A 16-row operand of one scale block, and the sum of one block's products.
-template <bool F8>
-struct Operand;
-template <>
-struct Operand<true> {
-  i32x8 v;
-  __device__ __forceinline__ void set(i32x8 c) { v = c; }
-};
-template <>
-struct Operand<false> {
+struct Operand {
   half8_t v[4];
   __device__ __forceinline__ void set(i32x8 c) { to_f16(c, v); }
 };
-__device__ __forceinline__ float4_t block_sum(const Operand<true> &a, const Operand<true> &b) {
-  return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a.v, b.v, float4_t{0.f, 0.f, 0.f, 0.f}, 0,
-                                                          0, 0, 0, 0, 0);
-}
-__device__ __forceinline__ float4_t block_sum(const Operand<false> &a, const Operand<false> &b) {
+__device__ __forceinline__ float4_t block_sum(const Operand &a, const Operand &b) {
   float4_t p = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
   for (int i = 0; i < 4; ++i) p = __builtin_amdgcn_mfma_f32_16x16x32_f16(a.v[i], b.v[i], p, 0, 0, 0);
@@ -163,7 +152,6 @@ gemm_f8b128_kernel(const uint8_t *__restrict__ W, const float *__restrict__ sw,
                    typename T::elem *__restrict__ Y, int64_t M, int64_t N, int64_t K, int tiles_m,
                    int tiles_n) {
   typedef Tile<BM, BN, WM, WN, WK, NS> C;
-  constexpr bool F8 = __is_same(T, TypeBF16);
   constexpr int TM = BM / WM / 16, TN = BN / WN / 16;  // 16 x 16 tiles of a wave
   constexpr int kScaleLoads = (BM + 63) / 64;          // waves of a group that bring scales of X
   static_assert((BM + BN) / 8 % C::kGroup == 0 && BN / WN <= 128 && 128 % (BN / WN) == 0, "tile");
@@ -267,15 +255,14 @@ gemm_f8b128_kernel(const uint8_t *__restrict__ W, const float *__restrict__ sw,
     for (int j = 0; j < TN; ++j) wraw[j] = frag(wst, wn + 16 * j + l16);
 #pragma unroll
     for (int i = 0; i < (kAhead == TM ? TM : 1); ++i) xraw[i] = frag(xst, wm + 16 * i + l16);
-    Operand<F8> wf[TN];
+    Operand wf[TN];
 #pragma unroll
     for (int j = 0; j < TN; ++j) wf[j].set(wraw[j]);
-    if constexpr (F8) __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
     for (int i = 0; i < TM; ++i) {
       if (kAhead != TM && i + 1 < TM) xraw[(i + 1) % kAhead] = frag(xst, wm + 16 * (i + 1) + l16);
       const float s = scales[wm + 16 * i + l16] * s_n;
-      Operand<F8> xf;
+      Operand xf;
       xf.set(xraw[i % kAhead]);
 #pragma unroll
       for (int j = 0; j < TN; ++j) {
@@ -285,16 +272,6 @@ gemm_f8b128_kernel(const uint8_t *__restrict__ W, const float *__restrict__ sw,
         p[j] = q;
       }
       s_prev = s;
-      if constexpr (F8) {
-        // matrix and vector instructions in turn
-        __builtin_amdgcn_sched_group_barrier(0x100, 3, 0);  // the next operand and a scale
-#pragma unroll
-        for (int j = 0; j < TN; ++j) {
-          __builtin_amdgcn_sched_group_barrier(0x8, 1, 0);
-          __builtin_amdgcn_sched_group_barrier(0x2, 4, 0);
-        }
-        __builtin_amdgcn_sched_barrier(0);
-      }
     }
   }
 #pragma unroll
@@ -342,7 +319,7 @@ gemm_f8b128_kernel(const uint8_t *__restrict__ W, const float *__restrict__ sw,
 // straight from memory to the operands, DEPTH blocks ahead, in registers.
 constexpr int kRowWaves = 8;
 
-template <class T, bool F8, int TM, int TN, int DEPTH>
+template <class T, int TM, int TN, int DEPTH>
 __global__ void __launch_bounds__(64 * kRowWaves)
 gemm_f8b128_rows_kernel(const uint8_t *__restrict__ W, const float *__restrict__ sw,
                         const uint8_t *__restrict__ X, const float *__restrict__ sx,
@@ -388,7 +365,7 @@ gemm_f8b128_rows_kernel(const uint8_t *__restrict__ W, const float *__restrict__
     s.sw = swr[kb];
   };
   auto operand = [&](const u32x4 (&v)[2]) {
-    Operand<F8> o;
+    Operand o;
     o.set(__builtin_bit_cast(i32x8, __builtin_shufflevector(v[0], v[1], 0, 1, 2, 3, 4, 5, 6, 7)));
     return o;
   };
@@ -419,12 +396,12 @@ gemm_f8b128_rows_kernel(const uint8_t *__restrict__ W, const float *__restrict__
             for (int i = 0; i < TM; ++i) s.x[i][u] = zero;
           }
       }
-      Operand<F8> w[TN];
+      Operand w[TN];
 #pragma unroll
       for (int j = 0; j < TN; ++j) w[j] = operand(s.w[j]);
 #pragma unroll
       for (int i = 0; i < TM; ++i) {
-        const Operand<F8> x = operand(s.x[i]);
+        const Operand x = operand(s.x[i]);
         const float f = s.sx[i] * s.sw;
 #pragma unroll
         for (int j = 0; j < TN; ++j) {
@@ -472,7 +449,7 @@ hipError_t launch_rows(const uint8_t *W, const float *sw, const uint8_t *X, cons
                        int64_t M, int64_t N, int64_t K, hipStream_t stream) {
   const int64_t tn = (N + 16 * TN - 1) / (16 * TN), tm = (M + 16 * TM - 1) / (16 * TM);
   if (tm * tn > 0x7fffffff) return hipErrorInvalidValue;
-  hipLaunchKernelGGL((gemm_f8b128_rows_kernel<T, __is_same(T, TypeBF16), TM, TN, DEPTH>),
+  hipLaunchKernelGGL((gemm_f8b128_rows_kernel<T, TM, TN, DEPTH>),
                      dim3((unsigned)(tm * tn)), dim3(64 * kRowWaves), 0, stream, W, sw, X, sx,
                      static_cast<typename T::elem *>(Y), M, N, K, (uint32_t)tn);
   return hipGetLastError();
@@ -483,8 +460,8 @@ hipError_t launch_gemm(const uint8_t *W, const float *sw, const uint8_t *X, cons
                        int64_t M, int64_t N, int64_t K, int num_cus, hipStream_t stream) {
   // Up to 16 rows: W is read once, by 16 of its rows a workgroup; by 64 when
   // that still gives most CUs one and X is worth sharing. Measured (K = 4096,
-  // us, 16 / 64 rows of W): M = 16, N = 4096 7.1 / 12.5, N = 14336 17.9 / 13.9,
-  // N = 28672 and K = 8192 63 / 54; M = 1, N = 28672 and K = 8192 42 / 50.
+  // us, 16 / 64 rows of W): M = 16, N = 4096 6.3 / 11.4, N = 14336 18.2 / 12.8,
+  // N = 28672 and K = 8192 52 / 42; M = 1, N = 28672 and K = 8192 36 / 39.
   if (M <= 16) {
     if (M > 4 && N >= 48 * (int64_t)num_cus)
       return launch_rows<T, 1, 4, 2>(W, sw, X, sx, Y, M, N, K, stream);
@@ -492,12 +469,12 @@ hipError_t launch_gemm(const uint8_t *W, const float *sw, const uint8_t *X, cons
   }
   // Else the kernel and tile whose estimated time is least: rounds over the
   // CUs times what a workgroup takes, a fixed part and one per scale block.
-  // The two parts (ns; the second for f8 / fp16 cores) were fitted to times
-  // at M = 24 .. 4096, N = 1001 .. 14336, K = 1040 and 4096; e.g. (us) 24 x
-  // 4127 x 4096 10.1 with 32 x 32 rows and 11.6 with 64 x 32 tiles, 200 x 4127
-  // x 1040 14.2 with 64 x 32 rows, 17.1 with 64 x 32 and 12.6 with 64 x 64
-  // tiles, 512 x 14336 x 4096 44 with 128 x 256 and 60 with 256 x 256 tiles.
-  constexpr bool F8 = __is_same(T, TypeBF16);
+  // The two parts (ns) were fitted to times at M = 24 .. 4096, N = 1001 ..
+  // 14336, K = 1040 and 4096; e.g. (us) 24 x 4127 x 4096 9.6 with 32 x 32 rows
+  // and 10.9 with 64 x 32 tiles, 200 x 4127 x 1040 11.9 with 64 x 32 rows, 16.2
+  // with 64 x 32 and 12.1 with 64 x 64 tiles, 512 x 14336 x 4096 67 with 128 x
+  // 256 and 77 with 64 x 64 tiles, 1024 x 4096 x 4096 34 with 128 x 128 and 61
+  // with 128 x 256 tiles.
   struct Choice {
     int bm, bn, per_cu, fixed, block;
   };
@@ -505,13 +482,12 @@ hipError_t launch_gemm(const uint8_t *W, const float *sw, const uint8_t *X, cons
       // W straight to registers, for few rows of X
       {32, 16, 1, 200, 170}, {32, 32, 1, 200, 250}, {48, 32, 1, 200, 350}, {64, 32, 1, 200, 420},
       // LDS tiles
-      {64, 32, 1, 2000, F8 ? 190 : 240}, {64, 64, 1, 3000, F8 ? 220 : 280},
-      {64, 64, 2, 2000, F8 ? 450 : 660}, {128, 128, 1, 3000, F8 ? 750 : 1100},
-      {128, 256, 1, 4000, F8 ? 1300 : 2050}, {256, 256, 1, 5000, F8 ? 2000 : 99999}};
+      {64, 32, 1, 2000, 240}, {64, 64, 1, 3000, 280}, {64, 64, 2, 2000, 660},
+      {128, 128, 1, 3000, 1100}, {128, 256, 1, 4000, 2050}};
   const int64_t blocks = (K + BK - 1) / BK;
   int best = -1;
   int64_t best_cost = 0;
-  for (int c = 0; c < 10; ++c) {
+  for (int c = 0; c < 9; ++c) {
     const Choice &o = kChoices[c];
     const int64_t tiles = ((M + o.bm - 1) / o.bm) * ((N + o.bn - 1) / o.bn);
     const int64_t slots = (int64_t)o.per_cu * num_cus;
@@ -533,8 +509,6 @@ hipError_t launch_gemm(const uint8_t *W, const float *sw, const uint8_t *X, cons
     case 7: return launch_tile<T, 128, 128, 2, 2, 2, 2>(W, sw, X, sx, Y, M, N, K, stream);
     case 8: return launch_tile<T, 128, 256, 2, 4, 1, 3>(W, sw, X, sx, Y, M, N, K, stream);
   }
-  // (fp16 cores: never the best, their operands do not fit beside 256 x 256 sums)
-  if constexpr (F8) return launch_tile<T, 256, 256, 2, 4, 1, 2>(W, sw, X, sx, Y, M, N, K, stream);
   return hipErrorInvalidValue;
 }
 

@@ -184,3 +184,42 @@ def test_rows_of_no_sequence(lens, news, max_q, before, after, hq, hkv, d, prefi
     live = of >= 0
     assert (out[~live] == 0).all() and np.isneginf(lse[~live]).all()
     compare(out[live], lse[live], [w[of[live]] for w in (wo, wl, bo, bl)], np.zeros(live.sum(), dtype=bool))
+
+
+# ---- 8-bit float products: sums in 32 bits ---------------------------------------
+@pytest.mark.parametrize("t", ["bf16", "f16", "f32"])
+@pytest.mark.parametrize("kind", ["outlier", "cancel"])
+@pytest.mark.parametrize("M, N, K", [
+    (1, 130, 272), (16, 130, 400), (9, 12301, 272), (20, 300, 144), (32, 4000, 272), (45, 4127, 400),
+    (64, 3000, 1040), (100, 1001, 272), (300, 3000, 400), (700, 8300, 272), (1500, 9000, 272),
+    (2900, 9100, 400),
+])
+def test_f8_sums_keep_small_products(M, N, K, kind, t):
+    """Products far below a block's largest count in full, for every output type
+    and tile: behind one large product, and behind two that cancel. Bound of each
+    output: half a step of the type, and for the fp32 sum of a block's 128 products
+    and of the blocks, in any order, 2^-23 of the sum of absolute products for
+    each addition and scaling."""
+    r = np.random.default_rng(M + N)
+    x, w = r.choice([1.75, 2.0], (M, K)), r.choice([3.5, 3.75], (N, K))
+    for k in range(0, K, 128):
+        at = k + r.permutation(min(128, K - k))[:2]
+        x[:, at[0]], w[:, at[0]] = 448.0, 448.0
+        if kind == "cancel":
+            x[:, at[1]], w[:, at[1]] = 448.0, -448.0
+    s = 2.0 ** -9  # (fp16 outputs stay in range)
+    nb, kb = -(-N // 128), -(-K // 128)
+    ws, xs = s * np.exp2(r.integers(0, 2, (nb, kb))), np.exp2(r.integers(0, 2, (kb, M)))
+    announce(f"gemm_f8b128 {kind} {M}x{N}x{K} {t}")
+    dev = lambda a: torch.from_numpy(a).to(DEV)  # noqa: E731
+    X, W = dev(x), dev(w)
+    f8 = torch.float8_e4m3fn
+    got = bq.lqmm_gemm_f8b128(W.to(f8), dev(ws).float(), X.to(f8), dev(xs).float(), out_dtype=DT[t]).double()
+    of = torch.arange(K, device=DEV) // 128
+    X, W = X * dev(xs)[of].t(), W * dev(ws)[torch.arange(N, device=DEV) // 128][:, of]
+    want = torch.matmul(X, W.t().contiguous())
+    total = torch.matmul(X.abs(), W.abs().t().contiguous())
+    sums = (128 + kb + 4) * 2.0 ** -23 * total
+    bound = so.U[t] * torch.exp2(torch.floor(torch.log2(want.abs() + sums))) + sums
+    over = (got - want).abs() - bound
+    assert torch.isfinite(got).all() and float(over.max()) <= 0, float(over.max())
