@@ -23,10 +23,12 @@
 // tell: maxima leave NaN out, so that a row whose every logit is NaN has it too,
 // with a sum of NaN, which has to reach the output.
 //
-// P is rounded to the cache's 16-bit type, as the matrix cores want it; in
-// fp16 it is kept at 2^kShift times its value, so that weights down to
-// 2^-(24 + kShift) of the largest do not vanish. Logits, maxima, sums and O
-// are fp32.
+// P is rounded to the cache's 16-bit type, as the matrix cores want it, and
+// kept at 2^kShift times its value. In fp16 that is up, so that weights down to
+// 2^-(24 + kShift) of the largest do not vanish (values of fp16 are far from
+// overflowing O); in bf16, whose values may be as large as an fp32, it is down:
+// a work item's at most 2^13 weights add up to less than 1, and so does O to
+// less than the largest value. Logits, maxima, sums and O are fp32.
 //
 // Two kernels. Few rows (one new token's heads) are bound by reading the
 // cache: 16 rows a workgroup, the waves take different keys, straight from
@@ -42,7 +44,10 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kRows = 16;          // rows of a work item
 constexpr int kStep = 32;          // keys of one step of a wave
-constexpr float kShift = 14.0f;    // weights are held as 2^14 times their value
+// log2 of what weights are held at, times their value
+template <class T>
+constexpr float kShift = __is_same(T, TypeF16) ? 14.0f : -14.0f;
+constexpr float kAloneShift = -14.0f;  // of rows done by themselves, in fp32
 constexpr int kMaxIds = kAttnMaxChunk / 8 + 8;
 
 // The part of a sequence's (or the prefix's) problem that one workgroup does.
@@ -238,7 +243,7 @@ __device__ __forceinline__ void row_alone(const AttnPrefix &a, const Item &it, i
     float mn = fmaxf(m, z);
     for (int s = 32; s > 0; s >>= 1) mn = fmaxf(mn, __shfl_xor(mn, s));
     const float c = m == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(m - mn);
-    const float e = __builtin_amdgcn_exp2f(z - (mn == -INFINITY ? 0.f : mn));
+    const float e = __builtin_amdgcn_exp2f(z - (mn == -INFINITY ? 0.f : mn) + kAloneShift);
     float sum = e;
     for (int s = 32; s > 0; s >>= 1) sum += __shfl_xor(sum, s);
     m = mn;
@@ -267,8 +272,8 @@ __device__ __forceinline__ void row_alone(const AttnPrefix &a, const Item &it, i
     else a.part_o[at * D + d] = o[u];
   }
   if (lane) return;
-  if (!direct) a.part_ml[at] = make_float2(m, l);
-  else if (a.lse) a.lse[flat] = l == 0.f ? -INFINITY : (m + __log2f(l)) * 0.6931471805599453f;
+  if (!direct) a.part_ml[at] = make_float2(m - kAloneShift, l);
+  else if (a.lse) a.lse[flat] = l == 0.f ? -INFINITY : (m - kAloneShift + __log2f(l)) * 0.6931471805599453f;
 }
 
 // ---- few rows -------------------------------------------------------------------
@@ -396,7 +401,7 @@ __device__ __forceinline__ void rows16_body(const AttnPrefix &a, const Item &it,
     float top = fmaxf(fmaxf(fmaxf(z[0][0], z[0][1]), fmaxf(z[0][2], z[0][3])),
                       fmaxf(fmaxf(z[1][0], z[1][1]), fmaxf(z[1][2], z[1][3])));
     const float mn = fmaxf(m, max_over_rows(top));
-    const float ref = (mn == -INFINITY ? 0.f : mn) - kShift;
+    const float ref = (mn == -INFINITY ? 0.f : mn) - kShift<T>;
     const float corr = __builtin_amdgcn_exp2f(m - mn);  // NaN only while m = mn = -inf
     const float c = m == -INFINITY ? 0.f : corr;
     m = mn;
@@ -495,9 +500,9 @@ __device__ __forceinline__ void rows16_body(const AttnPrefix &a, const Item &it,
   }
   if (owrite && out_d == 0) {
     if (direct) {
-      if (a.lse) a.lse[flat] = lj == 0.f ? -INFINITY : (mo - kShift + __log2f(lj)) * 0.6931471805599453f;
+      if (a.lse) a.lse[flat] = lj == 0.f ? -INFINITY : (mo - kShift<T> + __log2f(lj)) * 0.6931471805599453f;
     } else {
-      a.part_ml[it.part * nrows + flat] = make_float2(mo - kShift, lj);
+      a.part_ml[it.part * nrows + flat] = make_float2(mo - kShift<T>, lj);
     }
   }
 }
@@ -517,7 +522,9 @@ attn_rows16_kernel(AttnPrefix a, uint32_t item0) {
 // A running maximum that grows by no more than kSlack (log2) is left where it
 // is: O is rescaled when a row needs it, not at every step.
 constexpr float kSlack = 8.0f;
-constexpr float kWideShift = 6.0f;  // weights are at most 2^(kSlack + kWideShift), in fp16's range
+// Weights are at most 2^(kSlack + kWideShift): 2^kShift.
+template <class T>
+constexpr float kWideShift = kShift<T> - kSlack;
 
 // Waves of a SIMD that the wide kernel's registers leave room for: two of 32
 // rows, one of 64 rows (two at 64 dimensions) or of 256 dimensions.
@@ -680,7 +687,7 @@ __device__ __forceinline__ void wide_body(const AttnPrefix &a, const Item &it, u
 
   float16_t o[R][kDT];
   float m[R], l[R], top[R];
-  float ref[R];  // m - kWideShift, finite
+  float ref[R];  // m - kWideShift<T>, finite
 #pragma unroll
   for (int w = 0; w < R; ++w) {
     m[w] = top[w] = -INFINITY;
@@ -736,7 +743,7 @@ __device__ __forceinline__ void wide_body(const AttnPrefix &a, const Item &it, u
         const float mn = fmaxf(m[w], top[w]);
         const float c = m[w] == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(m[w] - mn);
         m[w] = mn;
-        ref[w] = (mn == -INFINITY ? 0.f : mn) - kWideShift;
+        ref[w] = (mn == -INFINITY ? 0.f : mn) - kWideShift<T>;
         l[w] *= c;
 #pragma unroll
         for (int i = 0; i < kDT; ++i)
@@ -905,7 +912,7 @@ __device__ __forceinline__ void wide_body(const AttnPrefix &a, const Item &it, u
               vec4{(elem)(o[w][i][r] * inv), (elem)(o[w][i][r + 1] * inv),
                    (elem)(o[w][i][r + 2] * inv), (elem)(o[w][i][r + 3] * inv)};
       if (h == 0 && a.lse)
-        a.lse[flat[w]] = sum == 0.f ? -INFINITY : (m[w] - kWideShift + __log2f(sum)) * 0.6931471805599453f;
+        a.lse[flat[w]] = sum == 0.f ? -INFINITY : (m[w] - kWideShift<T> + __log2f(sum)) * 0.6931471805599453f;
     } else {
       float *dst = a.part_o + (it.part * nrows + flat[w]) * D + 4 * h;
 #pragma unroll
@@ -914,7 +921,7 @@ __device__ __forceinline__ void wide_body(const AttnPrefix &a, const Item &it, u
         for (int r = 0; r < 16; r += 4)
           *reinterpret_cast<float4_t *>(dst + 32 * i + 2 * r) =
               float4_t{o[w][i][r], o[w][i][r + 1], o[w][i][r + 2], o[w][i][r + 3]};
-      if (h == 0) a.part_ml[it.part * nrows + flat[w]] = make_float2(m[w] - kWideShift, sum);
+      if (h == 0) a.part_ml[it.part * nrows + flat[w]] = make_float2(m[w] - kWideShift<T>, sum);
     }
   }
 }
@@ -929,6 +936,10 @@ attn_wide_kernel(AttnPrefix a, uint32_t item0) {
   if (find_item(a, idx, 32 * R * NW, it))
     wide_body<T, D, NW, R>(a, it, item0, smem);
 }
+
+// Parts are weighed by at most 2^-kJoinShift, so that the sum of any number of
+// them (under 2^19) stays below the largest value, as each does.
+constexpr float kJoinShift = 18.0f;
 
 // Joins the partial results of each row: D / 4 threads a row, four
 // dimensions each.
@@ -946,6 +957,7 @@ attn_join_kernel(AttnPrefix a) {
   float m = -INFINITY;
 #pragma unroll 4
   for (int p = 0; p < parts; ++p) m = fmaxf(m, a.part_ml[p * nrows + row].x);
+  m += kJoinShift;
   float l = 0.f;
   float4_t o = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll 4

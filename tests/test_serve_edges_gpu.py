@@ -223,3 +223,26 @@ def test_f8_sums_keep_small_products(M, N, K, kind, t):
     bound = so.U[t] * torch.exp2(torch.floor(torch.log2(want.abs() + sums))) + sums
     over = (got - want).abs() - bound
     assert torch.isfinite(got).all() and float(over.max()) <= 0, float(over.max())
+
+
+# ---- very large values -----------------------------------------------------------
+@pytest.mark.parametrize("again", [False, True])
+@pytest.mark.parametrize("case", [c[:6] + ("bf16",) for c in SHAPES] + [([9000], [1], 1, 1, 64, 0, "bf16")])
+def test_values_near_the_type_s_largest(case, again):
+    """The mean of finite values is finite: bf16 values up to 3.3e38, with and
+    without the rows of a mask's edge done by themselves."""
+    b = Batch(*case, "large values")
+    keep = ~np.isnan(np64(b.vc))
+    r = np.random.default_rng(1)
+    big = r.uniform(1e38, 3.3e38, b.vc.shape) * r.choice([-1.0, 1.0, 1.0, 1.0], b.vc.shape[-2])[:, None]
+    b.vc = torch.from_numpy(np.where(keep, big, np.nan)).to(DT["bf16"])
+    want = b.want()
+    rows = np.ones(len(b.q), dtype=bool)
+    if again:
+        if b.news[0] < 2:
+            pytest.skip("one new token")
+        page, place = b.keys_of(0, b.lens[0] - 1, b.lens[0])[0]
+        b.vc[page, :, place // 8, :, place % 8] = float("inf")
+        rows[b.start[1] - 1] = False  # sees the infinite value
+    out, lse = b.run()
+    compare(out[rows], lse[rows], [w[rows] for w in want], np.zeros(rows.sum(), dtype=bool))
