@@ -1,5 +1,7 @@
 """The served attention block at its edges: conversations that fill their pages,
 graphs and their prompts, workspaces of graphs and threads."""
+import gc
+
 import numpy as np
 import pytest
 
@@ -91,6 +93,7 @@ def test_a_call_keeps_no_workspace(where):
     args, kw, want = split_call(1)
     out, s = torch.empty_like(want), torch.cuda.Stream()
     torch.cuda.synchronize()
+    gc.collect()  # (what earlier tests left is not freed in between)
     before = torch.cuda.memory_allocated()
     for _ in range(3):
         if where == "default":  # (the stream's handle is 0)
