@@ -14,6 +14,8 @@ Usage: python -m block_quantized_matmul_amd.serve  (a small run on one GPU)
 """
 from __future__ import annotations
 
+import functools
+
 import numpy as np
 
 
@@ -107,7 +109,9 @@ class SharedPromptAttention:
 
     def capture(self, x):
         """A HIP graph of one step that reads x; returns (graph, output). Steps
-        taken before are kept; capturing takes none."""
+        taken before are kept; capturing takes none. The graph serves later
+        steps behind a prompt of the present length: its replay() raises
+        RuntimeError after a prompt() of another one."""
         torch = self.torch
         side = torch.cuda.Stream()
         side.wait_stream(torch.cuda.current_stream())
@@ -116,10 +120,29 @@ class SharedPromptAttention:
             self.step(x)
             self.lens.copy_(kept)
         torch.cuda.current_stream().wait_stream(side)
-        graph = torch.cuda.CUDAGraph()
+        graph = _step_graph_class()()
+        graph.layer, graph.prompt_len = self, self.prompt_len
         with torch.cuda.graph(graph, stream=side):
             out = self.step(x)
         return graph, out
+
+
+@functools.cache
+def _step_graph_class():
+    import torch
+
+    class StepGraph(torch.cuda.CUDAGraph):
+        """A graph of a step of `layer`. The prompt's length is part of what is
+        captured (it plans the attention's launches): the graph is good for that
+        length only."""
+
+        def replay(self):
+            if self.layer.prompt_len != self.prompt_len:
+                raise RuntimeError(f"the graph was captured behind a prompt of {self.prompt_len} tokens, "
+                                   f"which now has {self.layer.prompt_len}: capture it again")
+            super().replay()
+
+    return StepGraph
 
 
 def main():

@@ -2,7 +2,6 @@
 graphs and their prompts, workspaces of graphs and threads."""
 import gc
 
-import numpy as np
 import pytest
 
 import block_quantized_matmul_amd as bq
@@ -148,3 +147,30 @@ def test_threads_of_one_stream_do_not_share_a_workspace():
     for t in threads:
         t.join()
     assert wrong == [0, 0, 0]
+
+
+def test_a_graph_is_not_replayed_behind_another_prompt_length():
+    """A graph holds the prompt length of its capture: after a prompt of another
+    length its replay is refused, and takes no step; one captured then is right."""
+    layer, x_of = small_layer()
+    layer.prompt(x_of(17))
+    x = x_of(3)
+    announce("serving block: prompt after capture")
+    graph, _ = layer.capture(x)
+    graph.replay()
+    layer.prompt(x_of(23))
+    torch.cuda.synchronize()
+    before = layer.lens.tolist()
+    with pytest.raises(RuntimeError, match="prompt"):
+        graph.replay()
+    torch.cuda.synchronize()
+    assert layer.lens.tolist() == before
+    graph, out = layer.capture(x)
+    eager = layer.step(x).clone()
+    layer.lens -= 1
+    graph.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(out, eager)
+    layer.prompt(x_of(23))  # the same length: the graph stays good
+    graph.replay()
+    torch.cuda.synchronize()
