@@ -945,12 +945,12 @@ constexpr float kJoinShift = 18.0f;
 // dimensions each.
 template <class T, int D>
 __global__ void __launch_bounds__(kThreads)
-attn_join_kernel(AttnPrefix a) {
+attn_join_kernel(AttnPrefix a, uint32_t first) {
   typedef typename T::elem elem;
   constexpr int kPer = D / 4;
   constexpr int kRowsPerBlock = kThreads / kPer;
   const int64_t nrows = a.tokens * a.n_q_heads;
-  const int64_t row = (int64_t)blockIdx.x * kRowsPerBlock + threadIdx.x / kPer;
+  const int64_t row = (int64_t)(first + blockIdx.x) * kRowsPerBlock + threadIdx.x / kPer;
   const int d = 4 * (threadIdx.x % kPer);
   if (threadIdx.x / kPer >= kRowsPerBlock || row >= nrows) return;
   const int parts = a.prefix_parts + a.suffix_parts;
@@ -989,9 +989,9 @@ hipError_t launch_wide(const AttnPrefix &a, int64_t item0, int64_t items, hipStr
   constexpr auto kern = attn_wide_kernel<T, D, NW, R>;
   const hipError_t e = ensure_max_lds<kern>(Wide<D>::kLds);
   if (e != hipSuccess) return e;
-  hipLaunchKernelGGL(kern, dim3((unsigned)items), dim3(64 * NW), Wide<D>::kLds, stream, a,
-                     (uint32_t)item0);
-  return hipGetLastError();
+  return launch_in_pieces(items, 64 * NW, [&](uint32_t first, unsigned n) {
+    hipLaunchKernelGGL(kern, dim3(n), dim3(64 * NW), Wide<D>::kLds, stream, a, (uint32_t)item0 + first);
+  });
 }
 
 // Workgroups of 256 rows are eight waves of 32, or four of 64 where the
@@ -1008,9 +1008,10 @@ hipError_t launch_items(const AttnPrefix &a, int wide, int64_t item0, int64_t it
     return hipErrorInvalidValue;
   }
   if (wide == 1) return launch_wide<T, D, 4, 1>(a, item0, items, stream);
-  hipLaunchKernelGGL((attn_rows16_kernel<T, D>), dim3((unsigned)items), dim3(kThreads), 0, stream, a,
-                     (uint32_t)item0);
-  return hipGetLastError();
+  return launch_in_pieces(items, kThreads, [&](uint32_t first, unsigned n) {
+    hipLaunchKernelGGL((attn_rows16_kernel<T, D>), dim3(n), dim3(kThreads), 0, stream, a,
+                       (uint32_t)item0 + first);
+  });
 }
 
 // The prefix's and the suffixes' items are launched together when they are of
@@ -1029,10 +1030,10 @@ hipError_t launch(const AttnPrefix &a, hipStream_t stream) {
   if (e != hipSuccess || a.prefix_parts + a.suffix_parts == 1) return e;
   constexpr int kRowsPerBlock = kThreads / (D / 4);
   const int64_t nrows = a.tokens * a.n_q_heads;
-  hipLaunchKernelGGL((attn_join_kernel<T, D>),
-                     dim3((unsigned)((nrows + kRowsPerBlock - 1) / kRowsPerBlock)), dim3(kThreads),
-                     0, stream, a);
-  return hipGetLastError();
+  return launch_in_pieces((nrows + kRowsPerBlock - 1) / kRowsPerBlock, kThreads,
+                          [&](uint32_t first, unsigned n) {
+    hipLaunchKernelGGL((attn_join_kernel<T, D>), dim3(n), dim3(kThreads), 0, stream, a, first);
+  });
 }
 
 template <class T>

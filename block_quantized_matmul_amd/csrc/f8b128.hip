@@ -49,10 +49,11 @@ __device__ __forceinline__ float max16(float v) {
 template <class T>
 __global__ void __launch_bounds__(kQuantThreads)
 quant_f8b128_kernel(const typename T::elem *__restrict__ X, int64_t ldx, uint8_t *__restrict__ Xq,
-                    float *__restrict__ xs, int64_t M, int64_t K, int blocks) {
+                    float *__restrict__ xs, int64_t M, int64_t K, int blocks, uint32_t first) {
   const int l16 = threadIdx.x & 15;
-  const int b = blockIdx.x % blocks;
-  const int64_t m = (int64_t)(blockIdx.x / blocks) * 16 + (threadIdx.x >> 4);
+  const uint32_t block = first + blockIdx.x;
+  const int b = block % blocks;
+  const int64_t m = (int64_t)(block / blocks) * 16 + (threadIdx.x >> 4);
   const int64_t k = (int64_t)b * 128 + 8 * l16;
   if (m >= M) return;  // whole 16-lane groups
   float x[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
@@ -149,8 +150,8 @@ template <class T, int BM, int BN, int WM, int WN, int WK, int NS>
 __global__ void __launch_bounds__(64 * WM * WN * WK)
 gemm_f8b128_kernel(const uint8_t *__restrict__ W, const float *__restrict__ sw,
                    const uint8_t *__restrict__ X, const float *__restrict__ sx,
-                   typename T::elem *__restrict__ Y, int64_t M, int64_t N, int64_t K, int tiles_m,
-                   int tiles_n) {
+                   typename T::elem *__restrict__ Y, int64_t M, int64_t N, int64_t K, uint32_t tiles_m,
+                   uint32_t tiles_n, uint32_t first) {
   typedef Tile<BM, BN, WM, WN, WK, NS> C;
   constexpr int TM = BM / WM / 16, TN = BN / WN / 16;  // 16 x 16 tiles of a wave
   constexpr int kScaleLoads = (BM + 63) / 64;          // waves of a group that bring scales of X
@@ -164,11 +165,11 @@ gemm_f8b128_kernel(const uint8_t *__restrict__ W, const float *__restrict__ sw,
   const int l16 = lane & 15, g = lane >> 4;
   // Workgroups go to the 8 XCDs in turn; consecutive tiles (the M tiles of one
   // W tile) are put on one XCD, whose L2 then holds the W tile once.
-  const uint32_t tiles = (uint32_t)tiles_m * tiles_n;
-  const uint32_t xcd = blockIdx.x % 8, q8 = tiles / 8, r8 = tiles % 8;
-  const uint32_t tile = xcd * q8 + (xcd < r8 ? xcd : r8) + blockIdx.x / 8;
-  const int64_t m0 = (int64_t)(tile % (uint32_t)tiles_m) * BM;
-  const int64_t n0 = (int64_t)(tile / (uint32_t)tiles_m) * BN;
+  const uint32_t tiles = tiles_m * tiles_n, block = first + blockIdx.x;
+  const uint32_t xcd = block % 8, q8 = tiles / 8, r8 = tiles % 8;
+  const uint32_t tile = xcd * q8 + (xcd < r8 ? xcd : r8) + block / 8;
+  const int64_t m0 = (int64_t)(tile % tiles_m) * BM;
+  const int64_t n0 = (int64_t)(tile / tiles_m) * BN;
   const int wm = (gw % WM) * (BM / WM), wn = (gw / WM) * (BN / WN);
   const int blocks = (int)((K + BK - 1) / BK), steps = (blocks + WK - 1) / WK;
   const uint32_t Ku = (uint32_t)K;
@@ -324,14 +325,15 @@ __global__ void __launch_bounds__(64 * kRowWaves)
 gemm_f8b128_rows_kernel(const uint8_t *__restrict__ W, const float *__restrict__ sw,
                         const uint8_t *__restrict__ X, const float *__restrict__ sx,
                         typename T::elem *__restrict__ Y, int64_t M, int64_t N, int64_t K,
-                        uint32_t tiles_n) {
+                        uint32_t tiles_n, uint32_t first) {
   constexpr int kN = 16 * TN, kM = 16 * TM, kLd = kN + 4;
   __shared__ __attribute__((aligned(16))) float part[kRowWaves][kM][kLd];
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int l16 = lane & 15, g = lane >> 4;
-  const int64_t n0 = (int64_t)(blockIdx.x % tiles_n) * kN;
-  const int64_t m0 = (int64_t)(blockIdx.x / tiles_n) * kM;
+  const uint32_t block = first + blockIdx.x;
+  const int64_t n0 = (int64_t)(block % tiles_n) * kN;
+  const int64_t m0 = (int64_t)(block / tiles_n) * kM;
   const int blocks = (int)((K + BK - 1) / BK);
   const int per = (blocks + kRowWaves - 1) / kRowWaves;
   const int kb0 = wave * per, kb1 = kb0 + per < blocks ? kb0 + per : blocks;
@@ -436,23 +438,23 @@ hipError_t launch_tile(const uint8_t *W, const float *sw, const uint8_t *X, cons
   constexpr int kLds = Tile<BM, BN, WM, WN, WK, NS>::kLds;
   constexpr auto kern = gemm_f8b128_kernel<T, BM, BN, WM, WN, WK, NS>;
   const int64_t tm = (M + BM - 1) / BM, tn = (N + BN - 1) / BN;
-  if (tm * tn > 0x7fffffff) return hipErrorInvalidValue;
   const hipError_t e = ensure_max_lds<kern>(kLds);
   if (e != hipSuccess) return e;
-  hipLaunchKernelGGL(kern, dim3((unsigned)(tm * tn)), dim3(64 * WM * WN * WK), kLds, stream, W, sw, X, sx,
-                     static_cast<typename T::elem *>(Y), M, N, K, (int)tm, (int)tn);
-  return hipGetLastError();
+  return launch_in_pieces(tm * tn, 64 * WM * WN * WK, [&](uint32_t first, unsigned n) {
+    hipLaunchKernelGGL(kern, dim3(n), dim3(64 * WM * WN * WK), kLds, stream, W, sw, X, sx,
+                       static_cast<typename T::elem *>(Y), M, N, K, (uint32_t)tm, (uint32_t)tn, first);
+  });
 }
 
 template <class T, int TM, int TN, int DEPTH>
 hipError_t launch_rows(const uint8_t *W, const float *sw, const uint8_t *X, const float *sx, void *Y,
                        int64_t M, int64_t N, int64_t K, hipStream_t stream) {
   const int64_t tn = (N + 16 * TN - 1) / (16 * TN), tm = (M + 16 * TM - 1) / (16 * TM);
-  if (tm * tn > 0x7fffffff) return hipErrorInvalidValue;
-  hipLaunchKernelGGL((gemm_f8b128_rows_kernel<T, TM, TN, DEPTH>),
-                     dim3((unsigned)(tm * tn)), dim3(64 * kRowWaves), 0, stream, W, sw, X, sx,
-                     static_cast<typename T::elem *>(Y), M, N, K, (uint32_t)tn);
-  return hipGetLastError();
+  return launch_in_pieces(tm * tn, 64 * kRowWaves, [&](uint32_t first, unsigned n) {
+    hipLaunchKernelGGL((gemm_f8b128_rows_kernel<T, TM, TN, DEPTH>), dim3(n), dim3(64 * kRowWaves), 0,
+                       stream, W, sw, X, sx, static_cast<typename T::elem *>(Y), M, N, K, (uint32_t)tn,
+                       first);
+  });
 }
 
 template <class T>
@@ -491,7 +493,7 @@ hipError_t launch_gemm(const uint8_t *W, const float *sw, const uint8_t *X, cons
     const Choice &o = kChoices[c];
     const int64_t tiles = ((M + o.bm - 1) / o.bm) * ((N + o.bn - 1) / o.bn);
     const int64_t slots = (int64_t)o.per_cu * num_cus;
-    if (tiles > 0x7fffffff) continue;  // more workgroups than a launch takes
+    if (tiles > 0xffffffffll) continue;  // (they are numbered in 32 bits)
     const int64_t cost = (tiles + slots - 1) / slots * (o.fixed + o.block * blocks);
     if (best < 0 || cost < best_cost) {
       best = c;
@@ -517,9 +519,10 @@ hipError_t launch_quant(const void *X, int64_t ldx, uint8_t *Xq, float *xs, int6
                         hipStream_t stream) {
   const int64_t blocks = (K + 127) / 128, rows = (M + 15) / 16;
   if (blocks * rows > 0x7fffffff) return hipErrorInvalidValue;
-  hipLaunchKernelGGL(quant_f8b128_kernel<T>, dim3((unsigned)(blocks * rows)), dim3(kQuantThreads), 0,
-                     stream, static_cast<const typename T::elem *>(X), ldx, Xq, xs, M, K, (int)blocks);
-  return hipGetLastError();
+  return launch_in_pieces(blocks * rows, kQuantThreads, [&](uint32_t first, unsigned n) {
+    hipLaunchKernelGGL(quant_f8b128_kernel<T>, dim3(n), dim3(kQuantThreads), 0, stream,
+                       static_cast<const typename T::elem *>(X), ldx, Xq, xs, M, K, (int)blocks, first);
+  });
 }
 
 }  // namespace

@@ -31,19 +31,20 @@ constexpr int kMaxPairs = 128;  // head_dim <= 256
 
 template <class TI, class TC, bool INTER>
 __global__ void __launch_bounds__(kThreads)
-kv_append_kernel(KvAppend a) {
+kv_append_kernel(KvAppend a, uint32_t first) {
   typedef typename TI::elem in_t;
   typedef typename TC::elem cache_t;
   const int tid = threadIdx.x;
+  const uint32_t block = first + blockIdx.x;
   const int D = a.head_dim;
   const int64_t nslots = a.num_pages << a.page_log2;
   const int64_t head_elems = (int64_t)D << a.page_log2;  // one head of one page
 
-  if ((int)blockIdx.x < a.rot_blocks) {
+  if ((int)block < a.rot_blocks) {
     // One token and up to heads_per_block of its q and K heads.
     __shared__ float cs[2][kMaxPairs];
-    const int64_t t = blockIdx.x / a.head_blocks;
-    const int h0 = (int)(blockIdx.x % a.head_blocks) * a.heads_per_block;
+    const int64_t t = block / a.head_blocks;
+    const int h0 = (int)(block % a.head_blocks) * a.heads_per_block;
     const int pairs = a.rot_dim / 2;
     if (pairs) {
       const uint64_t pos = (uint64_t)(int64_t)a.positions[t];
@@ -119,7 +120,7 @@ kv_append_kernel(KvAppend a) {
   // token inside such a group is skipped; any other is stored by itself.
   __shared__ int64_t slot[24];
   __shared__ int lead[16];
-  const int64_t t0 = (int64_t)((blockIdx.x - a.rot_blocks) / a.v_blocks) * 8;
+  const int64_t t0 = (int64_t)((block - a.rot_blocks) / a.v_blocks) * 8;
   if (tid < 22) {
     const int64_t t = t0 - 7 + tid;
     int64_t s = -1;
@@ -140,7 +141,7 @@ kv_append_kernel(KvAppend a) {
   // Two elements of one head per thread; the eight tokens' loads go out
   // together (a workgroup of scattered tokens waits for memory once).
   const int half = D / 2;
-  const int h = (int)((blockIdx.x - a.rot_blocks) % a.v_blocks) * (kThreads / half) + tid / half;
+  const int h = (int)((block - a.rot_blocks) % a.v_blocks) * (kThreads / half) + tid / half;
   const int d = 2 * (tid % half);
   if (tid / half >= kThreads / half || h >= a.n_kv_heads) return;
   const in_t *src = static_cast<const in_t *>(a.v) + t0 * a.ldv + (int64_t)h * D + d;
@@ -184,13 +185,12 @@ kv_append_kernel(KvAppend a) {
 
 template <class TI, class TC>
 hipError_t launch(const KvAppend &a, int64_t blocks, hipStream_t stream) {
-  if (a.interleaved)
-    hipLaunchKernelGGL((kv_append_kernel<TI, TC, true>), dim3((unsigned)blocks), dim3(kThreads), 0,
-                       stream, a);
-  else
-    hipLaunchKernelGGL((kv_append_kernel<TI, TC, false>), dim3((unsigned)blocks), dim3(kThreads), 0,
-                       stream, a);
-  return hipGetLastError();
+  return launch_in_pieces(blocks, kThreads, [&](uint32_t first, unsigned n) {
+    if (a.interleaved)
+      hipLaunchKernelGGL((kv_append_kernel<TI, TC, true>), dim3(n), dim3(kThreads), 0, stream, a, first);
+    else
+      hipLaunchKernelGGL((kv_append_kernel<TI, TC, false>), dim3(n), dim3(kThreads), 0, stream, a, first);
+  });
 }
 
 }  // namespace

@@ -151,6 +151,21 @@ bool device_cus(int *num_cus);
 
 enum class ElemType { F32, F16, BF16 };
 
+// Launches `blocks` workgroups of `threads` threads, launch(first, n) for n of
+// them from number `first` on. One launch counts its threads in 32 bits and
+// drops the rest without an error, so that very many go out in several. (Whole
+// multiples of the 8 XCDs, to which workgroups are handed in turn.)
+template <class F>
+hipError_t launch_in_pieces(int64_t blocks, int threads, F launch) {
+  const int64_t most = 0xffffffffll / threads & ~7ll;
+  for (int64_t first = 0; first < blocks; first += most) {
+    launch((uint32_t)first, (unsigned)(blocks - first < most ? blocks - first : most));
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
+  return hipSuccess;
+}
+
 // Keys and values into a paged cache with rotation (kv_append.hip). Strides
 // in elements; q and q_out are null with n_q_heads = 0 when there is no q.
 struct KvAppend {

@@ -246,3 +246,68 @@ def test_values_near_the_type_s_largest(case, again):
         rows[b.start[1] - 1] = False  # sees the infinite value
     out, lse = b.run()
     compare(out[rows], lse[rows], [w[rows] for w in want], np.zeros(rows.sum(), dtype=bool))
+
+
+# ---- more workgroups than one launch takes ---------------------------------------
+# (a launch counts its threads in 32 bits)
+@pytest.mark.parametrize("M, N", [(1, 2 ** 27 + 37), (2 ** 28 + 35, 1)])
+def test_f8_product_of_very_many_rows(M, N):
+    announce(f"gemm_f8b128 {M}x{N}x16")
+    g = torch.Generator(device=DEV)
+    g.manual_seed(3)
+    code = lambda n: torch.randint(0x30, 0x40, (n, 16), device=DEV, generator=g, dtype=torch.uint8)  # noqa: E731
+    w, x = code(N), code(M)
+    ws, xs = torch.ones(-(-N // 128), 1, device=DEV), torch.ones(1, M, device=DEV)
+    y = bq.lqmm_gemm_f8b128(w, ws, x, xs, out_dtype=torch.float32).view(-1)
+    big, one = (w, x) if N > M else (x, w)
+    f8 = torch.float8_e4m3fn
+    for i in range(0, max(M, N), 2 ** 24):  # sums of products of 4 bits each: exact
+        want = (big[i:i + 2 ** 24].view(f8).float() * one.view(f8).float()).sum(1)
+        assert torch.equal(y[i:i + 2 ** 24], want)
+
+
+def test_quant_of_very_many_rows():
+    M = 2 ** 28 + 19
+    announce(f"quant {M}x16")
+    x = torch.empty(M, 16, dtype=torch.float16, device=DEV)
+    g = torch.Generator(device=DEV)
+    g.manual_seed(4)
+    for i in range(0, M, 2 ** 24):
+        x[i:i + 2 ** 24] = torch.randint(-7, 8, x[i:i + 2 ** 24].shape, device=DEV, generator=g, dtype=torch.int8)
+    x[:, 3] = 7.0  # the scale is 2^-6, and codes are exact
+    codes, scales = bq.lqmm_quant_f8b128(x)
+    assert (scales == 2.0 ** -6).all()
+    for i in range(0, M, 2 ** 24):
+        assert torch.equal(codes[i:i + 2 ** 24].float(), x[i:i + 2 ** 24].float() * 64)
+
+
+def test_append_of_very_many_tokens():
+    T, ps = 2 ** 24 + 11, 1024
+    P = -(-T // ps)
+    announce(f"append {T} tokens")
+    g = torch.Generator(device=DEV)
+    g.manual_seed(5)
+    k = torch.randint(-99, 100, (T, 1, 64), device=DEV, generator=g, dtype=torch.int16).half()
+    v = torch.randint(-99, 100, (T, 1, 64), device=DEV, generator=g, dtype=torch.int16).half()
+    kc, vc = (c.zero_() for c in bq.kv_cache_empty(P, 1, ps, 64))
+    bq.lqmm_kv_append(None, k, v, None, torch.arange(T, device=DEV), kc, vc)
+    assert torch.equal(kc.view(-1, 64)[:T], k.view(T, 64)) and not kc.view(-1, 64)[T:].any()
+    got = vc.view(-1, 64, 8).transpose(1, 2).reshape(-1, 64)
+    assert torch.equal(got[:T], v.view(T, 64)) and not got[T:].any()
+
+
+def test_attention_of_very_many_sequences():
+    B, H = 2 ** 20 + 3, 16
+    announce(f"attn {B} sequences of one key, {H} heads")
+    kc, vc = bq.kv_cache_empty(3, H, 8, 64)
+    g = torch.Generator(device=DEV)
+    g.manual_seed(6)
+    for c in (kc, vc):
+        c.copy_(torch.randn(c.shape, device=DEV, generator=g))
+    pages = torch.randint(0, 3, (B, 1), device=DEV, generator=g, dtype=torch.int32)
+    lens = torch.ones(B, dtype=torch.int32, device=DEV)
+    q = torch.ones(B, H, 64, dtype=torch.float16, device=DEV)
+    out = bq.lqmm_attn_prefix(q, kc, vc, pages, lens)
+    values = vc[:, :, 0, :, 0]  # one key: its value
+    for i in range(0, B, 2 ** 17):
+        assert torch.equal(out[i:i + 2 ** 17], values[pages[i:i + 2 ** 17, 0].long()])
