@@ -139,7 +139,9 @@ void *stream_of(PyObject *o, const at::Tensor &t) {
     v = PyObject_CallFunctionObjArgs(g_raw_stream, i, nullptr);
     Py_DECREF(i);
   } else if (PyLong_Check(o)) {
-    return PyLong_AsVoidPtr(o);
+    const unsigned long long h = PyLong_AsUnsignedLongLong(o);
+    if (PyErr_Occurred()) throw Failed();  // (no handle: negative or too wide)
+    return reinterpret_cast<void *>((uintptr_t)h);
   } else {
     v = PyObject_GetAttrString(o, "cuda_stream");
   }

@@ -174,3 +174,16 @@ def test_a_graph_is_not_replayed_behind_another_prompt_length():
     layer.prompt(x_of(23))  # the same length: the graph stays good
     graph.replay()
     torch.cuda.synchronize()
+
+
+@pytest.mark.parametrize("bad", [1 << 64, 1 << 90, -1, -(1 << 70)])
+def test_numbers_that_are_no_stream_handle_are_refused(bad):
+    """An integer outside a pointer's range raises, and nothing runs."""
+    announce(f"stream handle {bad}")
+    x = torch.ones(3, 128, device="cuda")
+    codes = torch.full((3, 128), 9, dtype=torch.uint8, device="cuda")
+    scales = torch.full((1, 3), 9.0, device="cuda")
+    with pytest.raises(OverflowError):
+        bq.lqmm_quant_f8b128(x, out=codes, scales=scales, stream=bad)
+    torch.cuda.synchronize()
+    assert (codes == 9).all() and (scales == 9).all()
