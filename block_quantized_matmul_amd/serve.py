@@ -54,6 +54,11 @@ class SharedPromptAttention:
         i32 = dict(dtype=torch.int32, device=self.dev)
         self.prompt_pages = torch.arange(prompt_pages, **i32)
         self.pages = (prompt_pages + torch.arange(batch * max_pages, **i32)).view(batch, max_pages)
+        # a conversation's slots in order, and behind the last the -1 that is not
+        # appended (of the pages above, which stay as they are)
+        self.slots = torch.full((batch, max_pages * page_size + 1), -1, device=self.dev)
+        self.slots[:, :-1] = (self.pages.long()[:, :, None] * page_size
+                              + torch.arange(page_size, device=self.dev)).view(batch, -1)
         self.lens = torch.zeros(batch, **i32)
         self.prompt_len = 0
         self.rows = torch.arange(batch, device=self.dev)
@@ -92,17 +97,13 @@ class SharedPromptAttention:
         already fills its max_pages pages gets no token and keeps its length;
         its row of the output is NaN (lengths are known on the device only, so
         that neither an eager step nor a replayed one can raise)."""
-        torch = self.torch
         q, k, v = self._project(x)
-        most = self.pages.shape[1] * self.ps
-        n = self.lens.clamp(0, most).long()
-        full = n == most
-        at = (n // self.ps).clamp_(max=self.pages.shape[1] - 1)
-        slots = torch.add(n % self.ps, self.pages[self.rows, at], alpha=self.ps)
-        slots.masked_fill_(full, -1)  # not appended
+        n = self.lens.clamp(0, self.slots.shape[1] - 1)
+        full = n == self.slots.shape[1] - 1
+        slots = self.slots[self.rows, n]
         q = self.bq.lqmm_kv_append(q, k, v, self.lens + self.prompt_len, slots, self.k_cache,
                                    self.v_cache, self.turns)
-        torch.add(n, ~full, out=self.lens)
+        self.torch.add(n, ~full, out=self.lens)
         o = self.bq.lqmm_attn_prefix(q, self.k_cache, self.v_cache, self.pages, self.lens,
                                      prefix_pages=self.prompt_pages, prefix_len=self.prompt_len)
         return self._output(o).masked_fill_(full[:, None], float("nan"))
