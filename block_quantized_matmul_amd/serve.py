@@ -6,9 +6,11 @@ behind one shared prompt, from the library's serving operators:
   (lqmm_kv_append) -> attention, the shared prompt's keys read once for the
   whole batch (lqmm_attn_prefix) -> e4m3 -> output product.
 
-Every buffer a decode step uses is allocated when the block is built, and the
-step reads its lengths and pages from device tensors, so that one captured HIP
-graph serves every later step.
+The caches, tables and lengths are device tensors made when the block is built,
+and a step reads its lengths and pages from them, so that one captured HIP graph
+serves every later step behind a prompt of the same length. What a step computes
+(codes, scales, products, outputs, the attention's workspace) is allocated by
+torch, in a captured step from the graph's own memory.
 
 Usage: python -m block_quantized_matmul_amd.serve  (a small run on one GPU)
 """

@@ -281,7 +281,7 @@ lqmm_status lqmm_rope_turns(const double *inv_freq, int64_t n, uint64_t *turns);
  * n_q_heads 0: only k and v are appended. positions: one int32 per token.
  * slots: one int64 per token; a token whose slot is negative or past the cache
  * is not appended (its q is still rotated). Two tokens with the same slot
- * leave either one there. rope_turns: rotary_dim / 2 entries; rotary_dim is a
+ * leave a mixture of them there. rope_turns: rotary_dim / 2 entries; rotary_dim is a
  * multiple of 16, at most head_dim, and 0 (with NULL positions and
  * rope_turns) rotates nothing. Pair i of a head is elements (i, i +
  * rotary_dim / 2), or (2i, 2i + 1) when `interleaved` is not 0; elements from
@@ -319,10 +319,13 @@ lqmm_status lqmm_kv_append(const void *q, const void *k, const void *v, int in_t
  * for the second product and the output is rounded once. Lengths and page
  * numbers are read on the device and bounded there: a length is cut to what
  * max_pages pages hold, a page number outside the cache reads page 0. Memory
- * past a sequence's length is never used, whatever it holds; a NaN or infinity
- * in a key or value that some token of a sequence sees may reach the
- * sequence's other new tokens of the same call.
- * max_pages bounds the planned work: pass the batch's largest page count.
+ * past a sequence's length is never used, whatever it holds. A NaN or infinity
+ * in a key or value reaches the rows that see its key, and no others; a row with
+ * a logit that is NaN is NaN, in out and lse.
+ * The keys are split by what max_pages pages hold, since lengths are not known
+ * on the host: a table wider than the batch's longest sequence needs (as a
+ * captured graph has to pass) is correct, and slower, because parts without
+ * keys are planned, written and joined too.
  * workspace: lqmm_attn_prefix_workspace_bytes() bytes (partial results; need
  * not be zeroed; LQMM_ERR_WORKSPACE when smaller); calls that may overlap
  * must not share it. The result does not depend on timing.
