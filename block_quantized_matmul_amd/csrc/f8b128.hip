@@ -69,12 +69,20 @@ quant_f8b128_kernel(const typename T::elem *__restrict__ X, int64_t ldx, uint8_t
     // from q = x r (Markstein's theorem: the remainder is exact). Three
     // instructions a value; the compiler's division took about ten and half
     // of the kernel's time: 4000 x 8192 fp16 25.7 -> 19.2 us.
-    const float inv = 1.0f / scale;
+    // Of a very small group value and scale are taken 2^64 up first: the
+    // remainder would fall below fp32's smallest step.
+    float s = scale;
+    if (scale < 0x1p-64f) {
+      s *= 0x1p64f;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) x[i] *= 0x1p64f;
+    }
+    const float inv = 1.0f / s;
     float y[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       const float q = x[i] * inv;
-      y[i] = fmaf(fmaf(-q, scale, x[i]), inv, q);
+      y[i] = fmaf(fmaf(-q, s, x[i]), inv, q);
     }
     uint32_t w[2];
 #pragma unroll

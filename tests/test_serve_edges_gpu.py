@@ -311,3 +311,27 @@ def test_attention_of_very_many_sequences():
     values = vc[:, :, 0, :, 0]  # one key: its value
     for i in range(0, B, 2 ** 17):
         assert torch.equal(out[i:i + 2 ** 17], values[pages[i:i + 2 ** 17, 0].long()])
+
+
+# ---- activations to e4m3: very small groups --------------------------------------
+@pytest.mark.parametrize("lo, hi", [(-149, -120), (-126, -110), (-112, -90), (-90, -60), (-66, -55), (100, 127)])
+def test_quant_rounds_small_and_large_groups_correctly(lo, hi):
+    """Codes are those of the correctly rounded quotient, ties and their
+    neighbours included, whatever the group's exponent."""
+    r = np.random.default_rng(hi - lo)
+    x = np.ldexp(r.standard_normal((4096, 1024)), r.integers(lo, hi, (4096, 8)).repeat(128, 1))
+    x = np.clip(x, -3e38, 3e38).astype(np.float32)
+    v = np.sort(np.unique(np.abs(so.E4M3[np.isfinite(so.E4M3)])))
+    mid = ((v[:-1] + v[1:]) / 2).astype(np.float32)
+    for m in range(0, 4096, 2):
+        top = np.float32(np.ldexp(1 + r.random(), int(r.integers(lo, hi))))
+        s = max(np.float32(top / np.float32(448.0)), np.float32(2.0 ** -126))
+        t = r.choice(mid, 127) * s
+        up = np.nextafter(t, np.float32(np.inf))
+        t = np.choose(r.integers(0, 3, 127), (t, up, np.nextafter(t, np.float32(-np.inf))))
+        x[m, :127], x[m, 127] = np.clip(t, -top, top), top
+    announce(f"quant of groups of 2^{lo} .. 2^{hi}")
+    codes, scales = bq.lqmm_quant_f8b128(torch.from_numpy(x).to(DEV))
+    want, ws = so.quantize(x)
+    assert np.array_equal(scales.cpu().numpy(), ws)
+    assert np.array_equal(np64(codes), want)
