@@ -50,6 +50,14 @@ constexpr float kShift = __is_same(T, TypeF16) ? 14.0f : -14.0f;
 constexpr float kAloneShift = -14.0f;  // of rows done by themselves, in fp32
 constexpr int kMaxIds = kAttnMaxChunk / 8 + 8;
 
+// ln(2^ref l). The exponent of l goes to the reference first: log2(l) by itself
+// would be rounded at the size of the weights' scale.
+__device__ __forceinline__ float lse_of(float ref, float l) {
+  if (l == 0.f) return -INFINITY;
+  return (ref + (float)__builtin_amdgcn_frexp_expf(l) + __log2f(__builtin_amdgcn_frexp_mantf(l))) *
+         0.6931471805599453f;
+}
+
 // The part of a sequence's (or the prefix's) problem that one workgroup does.
 struct Item {
   int h;            // key head
@@ -242,8 +250,9 @@ __device__ __forceinline__ void row_alone(const AttnPrefix &a, const Item &it, i
     }
     float mn = fmaxf(m, z);
     for (int s = 32; s > 0; s >>= 1) mn = fmaxf(mn, __shfl_xor(mn, s));
-    const float c = m == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(m - mn);
-    const float e = __builtin_amdgcn_exp2f(z - (mn == -INFINITY ? 0.f : mn) + kAloneShift);
+    const float ref = (mn == -INFINITY ? 0.f : mn) - kAloneShift;
+    const float c = m == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(m - kAloneShift - ref);
+    const float e = __builtin_amdgcn_exp2f(z - ref);
     float sum = e;
     for (int s = 32; s > 0; s >>= 1) sum += __shfl_xor(sum, s);
     m = mn;
@@ -273,7 +282,7 @@ __device__ __forceinline__ void row_alone(const AttnPrefix &a, const Item &it, i
   }
   if (lane) return;
   if (!direct) a.part_ml[at] = make_float2(m - kAloneShift, l);
-  else if (a.lse) a.lse[flat] = l == 0.f ? -INFINITY : (m - kAloneShift + __log2f(l)) * 0.6931471805599453f;
+  else if (a.lse) a.lse[flat] = lse_of(m - kAloneShift, l);
 }
 
 // ---- few rows -------------------------------------------------------------------
@@ -402,7 +411,8 @@ __device__ __forceinline__ void rows16_body(const AttnPrefix &a, const Item &it,
                       fmaxf(fmaxf(z[1][0], z[1][1]), fmaxf(z[1][2], z[1][3])));
     const float mn = fmaxf(m, max_over_rows(top));
     const float ref = (mn == -INFINITY ? 0.f : mn) - kShift<T>;
-    const float corr = __builtin_amdgcn_exp2f(m - mn);  // NaN only while m = mn = -inf
+    // (between references, as they were rounded)
+    const float corr = __builtin_amdgcn_exp2f(m - kShift<T> - ref);
     const float c = m == -INFINITY ? 0.f : corr;
     m = mn;
     vec8 p;
@@ -448,7 +458,7 @@ __device__ __forceinline__ void rows16_body(const AttnPrefix &a, const Item &it,
 #pragma unroll
   for (int w = 0; w < NW; ++w) mj = fmaxf(mj, sm.wave_m[w][m16]);
   constexpr int kPer = 32 / NW;  // values of a row that a thread writes per pass
-  const float mine = m == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(m - mj);
+  const float mine = m == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(m - kShift<T> - (mj - kShift<T>));
   const int out_row = tid / (4 * NW), out_d = kPer * (tid % (4 * NW));
   // the row that this thread writes
   float lj = 0.f, mo = -INFINITY;
@@ -457,7 +467,7 @@ __device__ __forceinline__ void rows16_body(const AttnPrefix &a, const Item &it,
 #pragma unroll
   for (int w = 0; w < NW; ++w) {
     const float mw = sm.wave_m[w][out_row], lw = sm.wave_l[w][out_row];
-    lj += lw == 0.f ? 0.f : lw * __builtin_amdgcn_exp2f(mw - mo);
+    lj += lw == 0.f ? 0.f : lw * __builtin_amdgcn_exp2f(mw - kShift<T> - (mo - kShift<T>));
   }
   const int orow = it.row0 + out_row;
   const bool owrite = orow < it.rows;
@@ -500,7 +510,7 @@ __device__ __forceinline__ void rows16_body(const AttnPrefix &a, const Item &it,
   }
   if (owrite && out_d == 0) {
     if (direct) {
-      if (a.lse) a.lse[flat] = lj == 0.f ? -INFINITY : (mo - kShift<T> + __log2f(lj)) * 0.6931471805599453f;
+      if (a.lse) a.lse[flat] = lse_of(mo - kShift<T>, lj);
     } else {
       a.part_ml[it.part * nrows + flat] = make_float2(mo - kShift<T>, lj);
     }
@@ -741,9 +751,10 @@ __device__ __forceinline__ void wide_body(const AttnPrefix &a, const Item &it, u
 #pragma unroll
       for (int w = 0; w < R; ++w) {
         const float mn = fmaxf(m[w], top[w]);
-        const float c = m[w] == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(m[w] - mn);
+        const float to = (mn == -INFINITY ? 0.f : mn) - kWideShift<T>;
+        const float c = m[w] == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(ref[w] - to);
         m[w] = mn;
-        ref[w] = (mn == -INFINITY ? 0.f : mn) - kWideShift<T>;
+        ref[w] = to;
         l[w] *= c;
 #pragma unroll
         for (int i = 0; i < kDT; ++i)
@@ -911,8 +922,7 @@ __device__ __forceinline__ void wide_body(const AttnPrefix &a, const Item &it, u
           *reinterpret_cast<vec4 *>(dst + 32 * i + 2 * r) =
               vec4{(elem)(o[w][i][r] * inv), (elem)(o[w][i][r + 1] * inv),
                    (elem)(o[w][i][r + 2] * inv), (elem)(o[w][i][r + 3] * inv)};
-      if (h == 0 && a.lse)
-        a.lse[flat[w]] = sum == 0.f ? -INFINITY : (m[w] - kWideShift<T> + __log2f(sum)) * 0.6931471805599453f;
+      if (h == 0 && a.lse) a.lse[flat[w]] = lse_of(m[w] - kWideShift<T>, sum);
     } else {
       float *dst = a.part_o + (it.part * nrows + flat[w]) * D + 4 * h;
 #pragma unroll
@@ -937,9 +947,10 @@ attn_wide_kernel(AttnPrefix a, uint32_t item0) {
     wide_body<T, D, NW, R>(a, it, item0, smem);
 }
 
-// Parts are weighed by at most 2^-kJoinShift, so that the sum of any number of
-// them (under 2^19) stays below the largest value, as each does.
-constexpr float kJoinShift = 18.0f;
+// Parts are weighed by at most 2^-18, so that the sum of any number of them
+// (under 2^19) stays below the largest value, as each does.
+constexpr int kJoinShift = 18;
+constexpr float kJoinWeight = 1.0f / (1 << kJoinShift);
 
 // Joins the partial results of each row: D / 4 threads a row, four
 // dimensions each.
@@ -957,7 +968,6 @@ attn_join_kernel(AttnPrefix a, uint32_t first) {
   float m = -INFINITY;
 #pragma unroll 4
   for (int p = 0; p < parts; ++p) m = fmaxf(m, a.part_ml[p * nrows + row].x);
-  m += kJoinShift;
   float l = 0.f;
   float4_t o = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll 4
@@ -966,7 +976,7 @@ attn_join_kernel(AttnPrefix a, uint32_t first) {
     const float2 ml = a.part_ml[p * nrows + row];
     const float4_t x = *reinterpret_cast<const float4_t *>(a.part_o + (p * nrows + row) * D + d);
     const bool seen = ml.y != 0.f;
-    const float w = seen ? __builtin_amdgcn_exp2f(ml.x - m) : 0.f;
+    const float w = seen ? __builtin_amdgcn_exp2f(ml.x - m) * kJoinWeight : 0.f;
     l += w * (seen ? ml.y : 0.f);
 #pragma unroll
     for (int r = 0; r < 4; ++r) o[r] += w * (seen ? x[r] : 0.f);
@@ -981,7 +991,7 @@ attn_join_kernel(AttnPrefix a, uint32_t first) {
 #pragma unroll
   for (int r = 0; r < 4; ++r) dst[r] = (elem)(o[r] * inv);
   if (a.lse && d == 0)
-    a.lse[row] = l == 0.f ? -INFINITY : (m + __log2f(l)) * 0.6931471805599453f;
+    a.lse[row] = lse_of(m, l * (1 << kJoinShift));
 }
 
 template <class T, int D, int NW, int R>

@@ -335,3 +335,16 @@ def test_quant_rounds_small_and_large_groups_correctly(lo, hi):
     want, ws = so.quantize(x)
     assert np.array_equal(scales.cpu().numpy(), ws)
     assert np.array_equal(np64(codes), want)
+
+
+# ---- lse --------------------------------------------------------------------------
+@pytest.mark.parametrize("t", ["f16", "bf16"])
+@pytest.mark.parametrize("scale", [0.0, 2.0 ** -24, 0.01])
+@pytest.mark.parametrize("case", [c[:6] for c in SHAPES])
+def test_lse_of_nearly_equal_logits(case, scale, t):
+    """lse has fp32's accuracy at its own size, whatever weights and parts are
+    scaled by: 2^-20 and 2^-22 of it beside the logits' error."""
+    b = Batch(*case, t, f"lse at scale {scale}")
+    want = so.attention(np64(b.q), np64(b.kc), np64(b.vc), b.table, b.lens, b.pids, b.prefix, b.start, scale, t)
+    out, lse = b.run(scale=scale)
+    compare(out, lse, want, np.zeros(len(b.q), dtype=bool))
