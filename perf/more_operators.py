@@ -23,7 +23,7 @@ TYPES = {"f16": torch.float16, "bf16": torch.bfloat16, "f32": torch.float32}
 F8 = torch.float8_e4m3fn
 E8 = torch.float8_e8m0fnu
 F8_MAX = 448.0
-E_MIN, E_MAX = -100, {"f16": 7, "bf16": 100}  # exponents of the 8-bit cache's scales
+E_MIN, E_MAX = -60, {"f16": 7, "bf16": 60}  # exponents of the 8-bit cache's scales
 EPS = 1e-6
 
 
