@@ -31,6 +31,8 @@ __all__ = [
     "lqmm_gemv_workspace_bytes", "lqmm_status_string", "lqmm_version",
     "lqmm_rope_turns", "lqmm_kv_append", "lqmm_attn_prefix", "lqmm_attn_prefix_workspace_bytes",
     "lqmm_gemm_f8b128", "lqmm_quant_f8b128", "kv_cache_empty",
+    "lqmm_kv_append_norm", "lqmm_kv_read_f8", "lqmm_attn_prefix_f8",
+    "lqmm_attn_prefix_f8_workspace_bytes", "lqmm_quant_mxfp4", "lqmm_gemm_mxfp4", "kv_scales_empty",
     "Q4_0_BLOCK_BYTES", "Q8_0_BLOCK_BYTES", "Q4_K_BLOCK_BYTES", "Q6_K_BLOCK_BYTES",
     "Q2_K_BLOCK_BYTES", "Q1_0_BLOCK_BYTES",
 ]
@@ -52,7 +54,9 @@ EXPORTS = ("lqmm_sgemm", "lqmm_gemv_q4_0", "lqmm_gemv_q4_0_noalloc", "lqmm_gemm_
            "lqmm_gemv_q1_0", "lqmm_gemv_i4g32", "lqmm_gemm_q4_0_f16", "lqmm_gemm_q4_k_f16",
            "lqmm_gemv_workspace_bytes", "lqmm_status_string", "lqmm_version",
            "lqmm_rope_turns", "lqmm_kv_append", "lqmm_attn_prefix",
-           "lqmm_attn_prefix_workspace_bytes", "lqmm_gemm_f8b128", "lqmm_quant_f8b128")
+           "lqmm_attn_prefix_workspace_bytes", "lqmm_gemm_f8b128", "lqmm_quant_f8b128",
+           "lqmm_kv_append_norm", "lqmm_kv_read_f8", "lqmm_attn_prefix_f8",
+           "lqmm_attn_prefix_f8_workspace_bytes", "lqmm_quant_mxfp4", "lqmm_gemm_mxfp4")
 
 
 class LqmmError(RuntimeError):
@@ -106,8 +110,18 @@ def load():
     lib.lqmm_attn_prefix_workspace_bytes.restype = sz
     lib.lqmm_gemm_f8b128.argtypes = [p, p, p, p, p, ci, i64, i64, i64, p]
     lib.lqmm_quant_f8b128.argtypes = [p, ci, i64, p, p, i64, i64, p]
+    lib.lqmm_kv_append_norm.argtypes = ([p, p, p, ci] + [i64] * 3 + [p, p, p, i64, ci, p, p, f32]
+                                        + [p] * 5 + [ci] + [i64] * 6 + [p])
+    lib.lqmm_kv_read_f8.argtypes = [p] * 5 + [i64, p, p, p, ci] + [i64] * 6 + [p]
+    lib.lqmm_attn_prefix_f8.argtypes = [p, i64, p, p, p, p, ci, p, i64, p, i64, p, p, i64, p, p, f32,
+                                        *[i64] * 7, p, sz, p]
+    lib.lqmm_attn_prefix_f8_workspace_bytes.argtypes = [i64] * 9
+    lib.lqmm_attn_prefix_f8_workspace_bytes.restype = sz
+    lib.lqmm_quant_mxfp4.argtypes = [p, ci, i64, p, p, i64, i64, p]
+    lib.lqmm_gemm_mxfp4.argtypes = [p, p, p, p, p, ci, i64, i64, i64, p]
     for name in ("lqmm_rope_turns", "lqmm_kv_append", "lqmm_attn_prefix", "lqmm_gemm_f8b128",
-                 "lqmm_quant_f8b128"):
+                 "lqmm_quant_f8b128", "lqmm_kv_append_norm", "lqmm_kv_read_f8",
+                 "lqmm_attn_prefix_f8", "lqmm_quant_mxfp4", "lqmm_gemm_mxfp4"):
         getattr(lib, name).restype = st
     lib.lqmm_status_string.argtypes = [ctypes.c_int]
     lib.lqmm_status_string.restype = ctypes.c_char_p
@@ -435,6 +449,17 @@ def kv_cache_empty(num_pages, n_kv_heads, page_size, head_dim, dtype=None, devic
     return k, v
 
 
+def kv_scales_empty(num_pages, n_kv_heads, page_size, device="cuda"):
+    """(k_scales, v_scales) of an 8-bit cache (kv_cache_empty with torch's
+    float8_e4m3fn): float8_e8m0fnu, all 1."""
+    torch = _torch()
+    if page_size % 8:
+        raise ValueError("page_size must be a multiple of 8")
+    k, v = (torch.full((num_pages, n_kv_heads, page_size), 127, dtype=torch.uint8, device=device)
+            .view(torch.float8_e8m0fnu) for _ in range(2))
+    return k, v
+
+
 def lqmm_rope_turns(inv_freq, device="cuda"):
     """The rotation table of lqmm_kv_append: inv_freq (radians per position, any
     sequence or host array) as 64-bit fractions of a turn, an int64 tensor on
@@ -496,3 +521,62 @@ def lqmm_gemm_f8b128(W, wscale, Xq, xscale, out=None, out_dtype=None, stream=Non
     (ceil(K / 128), M) as lqmm_quant_f8b128 makes them. out_dtype: float16
     (default), bfloat16 or float32."""
     return _calls().gemm_f8b128(W, wscale, Xq, xscale, out, out_dtype, stream)
+
+
+# ---- serving operators in fewer bits -------------------------------------------
+# Codes of an 8-bit cache are float8_e4m3fn (or uint8) tensors, its scales and
+# those of 4-bit floats float8_e8m0fnu (or uint8).
+
+def lqmm_kv_append_norm(q, k, v, positions, slots, k_cache, v_cache, k_scales=None, v_scales=None,
+                        q_norm=None, k_norm=None, eps=1e-6, rope_turns=None, interleaved=False,
+                        q_out=None, stream=None):
+    """lqmm_kv_append with norms: each head of q and k becomes x / sqrt(mean(x^2)
+    + eps) * weight (q_norm, k_norm: float32 (head_dim,), None: no norm) before
+    the rotation. The caches are float16 or bfloat16, or 8-bit codes with
+    k_scales and v_scales (num_pages, n_kv_heads, page_size). Returns the
+    rotated q in the 16-bit caches' type; with 8-bit caches in q_out's, else in
+    k's when that is 16-bit, else float16 (None without q)."""
+    return _calls().kv_append_norm(q, k, v, positions, slots, k_cache, v_cache, k_scales, v_scales,
+                                   q_norm, k_norm, eps, rope_turns, interleaved, q_out, stream)
+
+
+def lqmm_kv_read_f8(k_cache, v_cache, k_scales, v_scales, pages, starts, tokens, dtype=None,
+                    k_out=None, v_out=None, stream=None):
+    """The 8-bit cache back to dense rows: row starts[b] + j (int32, batch + 1
+    entries, not decreasing) of the returned (k, v), (tokens, n_kv_heads,
+    head_dim) each, is token j of pages[b] (int32, (batch, max_pages)). Rows of
+    no sequence are zeros. dtype: float16 (default), bfloat16 or float32."""
+    return _calls().kv_read_f8(k_cache, v_cache, k_scales, v_scales, pages, starts, tokens, dtype,
+                               k_out, v_out, stream)
+
+
+def lqmm_attn_prefix_f8_workspace_bytes(prefix_len, max_pages, max_q, tokens, batch, n_q_heads,
+                                        n_kv_heads, head_dim, page_size) -> int:
+    return load().lqmm_attn_prefix_f8_workspace_bytes(
+        int(prefix_len), int(max_pages), int(max_q), int(tokens), int(batch), int(n_q_heads),
+        int(n_kv_heads), int(head_dim), int(page_size))
+
+
+def lqmm_attn_prefix_f8(q, k_cache, v_cache, k_scales, v_scales, pages, seq_lens, prefix_pages=None,
+                        prefix_len=0, q_start=None, max_q=1, scale=None, out=None, return_lse=False,
+                        lse=None, workspace=None, stream=None):
+    """lqmm_attn_prefix over an 8-bit cache (float8_e4m3fn codes with a scale for
+    each token and head); q and out are float16 or bfloat16. workspace: of
+    lqmm_attn_prefix_f8_workspace_bytes."""
+    return _calls().attn_prefix_f8(q, k_cache, v_cache, k_scales, v_scales, pages, seq_lens,
+                                   prefix_pages, prefix_len, q_start, max_q, scale, out, return_lse,
+                                   lse, workspace, stream)
+
+
+def lqmm_quant_mxfp4(X, out=None, scales=None, stream=None):
+    """X (M, K) float32, float16 or bfloat16 (rows may be strided, K % 32 == 0) to
+    microscaled 4-bit floats: (codes (M, K / 2) uint8, the first of a pair in the
+    low half, scales (M, K / 32) float8_e8m0fnu)."""
+    return _calls().quant_mxfp4(X, out, scales, stream)
+
+
+def lqmm_gemm_mxfp4(W, wscale, Xq, xscale, out=None, out_dtype=None, stream=None):
+    """Y (M, N) = X @ W^T over microscaled 4-bit floats: W (N, K / 2) uint8 with
+    wscale (N, K / 32), Xq (M, K / 2) with xscale (M, K / 32) as lqmm_quant_mxfp4
+    makes them. out_dtype: float16 (default), bfloat16 or float32."""
+    return _calls().gemm_mxfp4(W, wscale, Xq, xscale, out, out_dtype, stream)

@@ -205,6 +205,40 @@ void attn_prefix_plan(AttnPrefix &a, int64_t max_suffix, int num_cus);
 size_t attn_prefix_workspace(const AttnPrefix &a);
 hipError_t attn_prefix_launch(AttnPrefix &a, void *ws, ElemType type, hipStream_t stream);
 
+// The same with norms of the heads of q and k before the rotation, into a cache
+// of 16 bits or, with scales, of e4m3 codes (kv_append_norm.hip).
+struct KvAppendNorm : KvAppend {
+  const float *q_norm, *k_norm;    // head_dim weights; null: no norm
+  float eps;
+  uint8_t *k_scales, *v_scales;    // [page][head][token], null for 16 bits
+  int most_scale;                  // the largest scale byte
+};
+hipError_t kv_append_norm_launch(KvAppendNorm a, ElemType in, ElemType type, hipStream_t stream);
+
+// The 8-bit cache back to dense rows (kv_read_f8.hip).
+struct KvRead {
+  const uint8_t *k_cache, *v_cache, *k_scales, *v_scales;
+  const int32_t *pages, *starts;
+  void *k_out, *v_out;
+  int64_t batch, max_pages, tokens, num_pages;
+  int n_kv_heads, head_dim, page_log2;
+};
+hipError_t kv_read_f8_launch(const KvRead &a, ElemType type, hipStream_t stream);
+
+// Attention over the 8-bit cache (attn_f8.hip).
+struct AttnPrefixF8 : AttnPrefix {
+  const uint8_t *k_scales, *v_scales;
+};
+void attn_f8_plan(AttnPrefixF8 &a, int64_t max_suffix, int num_cus);
+hipError_t attn_f8_launch(AttnPrefixF8 &a, void *ws, ElemType type, hipStream_t stream);
+
+// Microscaled 4-bit floats (mxfp4.hip).
+hipError_t quant_mxfp4_launch(const void *X, ElemType type, int64_t ldx, uint8_t *Xq, uint8_t *xs,
+                              int64_t M, int64_t K, hipStream_t stream);
+hipError_t gemm_mxfp4_launch(const uint8_t *W, const uint8_t *sw, const uint8_t *X, const uint8_t *sx,
+                             void *Y, ElemType type, int64_t M, int64_t N, int64_t K, int num_cus,
+                             hipStream_t stream);
+
 // e4m3 codes with a scale per block of 128 (f8b128.hip).
 hipError_t quant_f8b128_launch(const void *X, ElemType type, int64_t ldx, uint8_t *Xq, float *xs,
                                int64_t M, int64_t K, hipStream_t stream);

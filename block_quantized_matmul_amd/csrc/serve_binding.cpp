@@ -96,8 +96,14 @@ struct Caches {
   int type;
 };
 
-Caches caches(PyObject *ko, PyObject *vo) {
+bool is_f8(const at::Tensor &t) {
+  return t.scalar_type() == at::kFloat8_e4m3fn || t.scalar_type() == at::kByte;
+}
+
+// f8: the 8-bit caches' codes (type 0); else 16-bit caches.
+Caches caches(PyObject *ko, PyObject *vo, bool f8 = false) {
   const at::Tensor &kt = tensor(ko, "k_cache");
+  if (f8 && !is_f8(kt)) type_error("%s must be float8_e4m3fn (or uint8)", "k_cache");
   const at::Tensor &k = whole(ko, kt.scalar_type(), "k_cache");
   const at::Tensor &v = whole(vo, kt.scalar_type(), "v_cache");
   if (k.dim() != 4) value_error("%s must be (num_pages, n_kv_heads, page_size, head_dim)", "k_cache");
@@ -106,11 +112,21 @@ Caches caches(PyObject *ko, PyObject *vo) {
       v.size(3) != d || v.size(4) != 8)
     value_error("%s must be (num_pages, n_kv_heads, page_size / 8, head_dim, 8)", "v_cache");
   same_device(k, v);
-  return {k, v, p, h, ps, d, type_code(k, "k_cache", false)};
+  return {k, v, p, h, ps, d, f8 ? 0 : type_code(k, "k_cache", false)};
 }
 
 bool has_shape(const at::Tensor &t, std::initializer_list<int64_t> want) {
   return t.sizes() == at::IntArrayRef(want.begin(), want.size());
+}
+
+// A contiguous device tensor of e8m0 scales (float8_e8m0fnu or raw bytes).
+const at::Tensor &scale_bytes(PyObject *o, std::initializer_list<int64_t> shape, const char *name) {
+  const at::Tensor &t = tensor(o, name);
+  if (t.scalar_type() != at::kFloat8_e8m0fnu && t.scalar_type() != at::kByte)
+    type_error("%s must be float8_e8m0fnu (or uint8)", name);
+  whole(o, t.scalar_type(), name);
+  if (!has_shape(t, shape)) value_error("%s has the wrong shape", name);
+  return t;
 }
 
 int64_t integer(PyObject *o, const char *name) {
@@ -190,11 +206,25 @@ bool arity(Py_ssize_t n, Py_ssize_t want) {
   return false;
 }
 
-PyObject *kv_append(PyObject *, PyObject *const *a, Py_ssize_t n) {
-  if (!arity(n, 11)) return nullptr;
+// What an append with norms takes beside lqmm_kv_append's arguments.
+struct Norms {
+  PyObject *k_scales, *v_scales, *q_norm, *k_norm, *eps;
+};
+
+const float *norm_weight(PyObject *o, const at::Tensor &like, int64_t dim, const char *name) {
+  if (o == Py_None) return nullptr;
+  const at::Tensor &t = whole(o, at::kFloat, name);
+  if (!has_shape(t, {dim})) value_error("%s must be (head_dim,)", name);
+  same_device(like, t);
+  return static_cast<const float *>(t.data_ptr());
+}
+
+// a: the arguments of lqmm_kv_append in order; norms: null for that call.
+PyObject *append(PyObject *const *a, const Norms *norms) {
   return guarded([&]() -> PyObject * {
     PyObject *qo = a[0], *po = a[3], *turns_o = a[7], *out_o = a[9];
-    const Caches c = caches(a[5], a[6]);
+    const bool f8 = norms && is_f8(tensor(a[5], "k_cache"));
+    const Caches c = caches(a[5], a[6], f8);
     const at::Tensor &k = tensor(a[1], "k"), &v = tensor(a[2], "v");
     const int64_t ldk = row_stride(k, c.heads, c.dim, "k"), ldv = row_stride(v, c.heads, c.dim, "v");
     const int64_t tokens = k.size(0);
@@ -220,6 +250,29 @@ PyObject *kv_append(PyObject *, PyObject *const *a, Py_ssize_t n) {
     }
     const int interleaved = PyObject_IsTrue(a[8]);
     if (interleaved < 0) throw Failed();
+    uint8_t *k_scales = nullptr, *v_scales = nullptr;
+    const float *q_norm = nullptr, *k_norm = nullptr;
+    double eps = 0.0;
+    if (norms) {
+      if (f8) {
+        const at::Tensor &ks = scale_bytes(norms->k_scales, {c.pages, c.heads, c.page_size}, "k_scales");
+        const at::Tensor &vs = scale_bytes(norms->v_scales, {c.pages, c.heads, c.page_size}, "v_scales");
+        same_device(k, ks);
+        same_device(k, vs);
+        k_scales = static_cast<uint8_t *>(ks.data_ptr());
+        v_scales = static_cast<uint8_t *>(vs.data_ptr());
+      } else if (norms->k_scales != Py_None || norms->v_scales != Py_None) {
+        value_error("%s belong to 8-bit caches", "scales");
+      }
+      if (qo != Py_None) q_norm = norm_weight(norms->q_norm, k, c.dim, "q_norm");
+      else if (norms->q_norm != Py_None) value_error("%s without q", "q_norm");
+      k_norm = norm_weight(norms->k_norm, k, c.dim, "k_norm");
+      eps = PyFloat_AsDouble(norms->eps);
+      if (eps == -1.0 && PyErr_Occurred()) throw Failed();
+    }
+    // the type of q_out: the 16-bit caches'; beside 8-bit ones its own, or k's
+    at::ScalarType q_type = f8 ? (type == LQMM_F32 ? at::kHalf : k.scalar_type()) : c.k.scalar_type();
+    if (f8 && out_o != Py_None) q_type = tensor(out_o, "q_out").scalar_type();
     const c10::DeviceGuard guard(k.device());
     int64_t heads = 0, ldq = 0;
     const void *qp = nullptr;
@@ -233,9 +286,9 @@ PyObject *kv_append(PyObject *, PyObject *const *a, Py_ssize_t n) {
         value_error("%s must have the same element type and tokens", "q and k");
       same_device(k, q);
       if (out_o == Py_None) {
-        out = at::empty({tokens, heads, c.dim}, c.k.options());
+        out = at::empty({tokens, heads, c.dim}, c.k.options().dtype(q_type));
       } else {
-        out = whole(out_o, c.k.scalar_type(), "q_out");
+        out = whole(out_o, q_type, "q_out");
         if (!has_shape(out, {tokens, heads, c.dim})) value_error("%s has the wrong shape", "q_out");
         same_device(k, out);
       }
@@ -245,7 +298,17 @@ PyObject *kv_append(PyObject *, PyObject *const *a, Py_ssize_t n) {
     }
     void *stream = stream_of(a[10], k);
     void *outp = out.defined() ? out.data_ptr() : nullptr;
+    int cache_type = c.type;
+    if (f8) cache_type = out.defined() ? type_code(out, "q_out", false) : q_type == at::kHalf ? LQMM_F16 : LQMM_BF16;
     check(call([&] {
+      if (norms)
+        return lqmm_kv_append_norm(qp, k.data_ptr(), v.data_ptr(), type, ldq, ldk, ldv,
+                                   static_cast<const int32_t *>(positions),
+                                   static_cast<const int64_t *>(slots.data_ptr()),
+                                   static_cast<const uint64_t *>(turns), rot, interleaved, q_norm,
+                                   k_norm, (float)eps, outp, c.k.data_ptr(), c.v.data_ptr(), k_scales,
+                                   v_scales, cache_type, tokens, heads, c.heads, c.dim, c.page_size,
+                                   c.pages, stream);
       return lqmm_kv_append(qp, k.data_ptr(), v.data_ptr(), type, ldq, ldk, ldv,
                             static_cast<const int32_t *>(positions),
                             static_cast<const int64_t *>(slots.data_ptr()),
@@ -258,15 +321,100 @@ PyObject *kv_append(PyObject *, PyObject *const *a, Py_ssize_t n) {
   });
 }
 
-PyObject *attn_prefix(PyObject *, PyObject *const *a, Py_ssize_t n) {
-  if (!arity(n, 15)) return nullptr;
+PyObject *kv_append(PyObject *, PyObject *const *a, Py_ssize_t n) {
+  if (!arity(n, 11)) return nullptr;
+  return append(a, nullptr);
+}
+
+PyObject *kv_append_norm(PyObject *, PyObject *const *a, Py_ssize_t n) {
+  if (!arity(n, 16)) return nullptr;
+  // (a norm's arguments stand between the caches and the rotation's table)
+  PyObject *plain[11] = {a[0], a[1], a[2], a[3], a[4], a[5], a[6], a[12], a[13], a[14], a[15]};
+  const Norms norms = {a[7], a[8], a[9], a[10], a[11]};
+  return append(plain, &norms);
+}
+
+// A pair of tensors as a Python tuple.
+PyObject *both_of(const at::Tensor &a, const at::Tensor &b) {
+  PyObject *p = THPVariable_Wrap(a), *s = THPVariable_Wrap(b);
+  PyObject *both = p && s ? PyTuple_Pack(2, p, s) : nullptr;
+  Py_XDECREF(p);
+  Py_XDECREF(s);
+  return both;
+}
+
+// A torch.dtype argument, or the given output's type, or float16.
+at::ScalarType out_type(PyObject *dtype, PyObject *out, const char *name) {
+  if (dtype != Py_None) {
+    if (!THPDtype_Check(dtype)) type_error("%s must be a torch.dtype", name);
+    return reinterpret_cast<THPDtype *>(dtype)->scalar_type;
+  }
+  return out != Py_None ? tensor(out, "out").scalar_type() : at::kHalf;
+}
+
+PyObject *kv_read_f8(PyObject *, PyObject *const *a, Py_ssize_t n) {
+  if (!arity(n, 11)) return nullptr;
+  return guarded([&]() -> PyObject * {
+    const Caches c = caches(a[0], a[1], true);
+    const at::Tensor &ks = scale_bytes(a[2], {c.pages, c.heads, c.page_size}, "k_scales");
+    const at::Tensor &vs = scale_bytes(a[3], {c.pages, c.heads, c.page_size}, "v_scales");
+    const at::Tensor &pages = whole(a[4], at::kInt, "pages"), &starts = whole(a[5], at::kInt, "starts");
+    if (pages.dim() != 2 || starts.numel() != pages.size(0) + 1)
+      value_error("%s must be (batch, max_pages) and starts (batch + 1,)", "pages");
+    const int64_t tokens = integer(a[6], "tokens");
+    if (tokens <= 0) value_error("%s must be positive", "tokens");
+    same_device(c.k, ks);
+    same_device(c.k, vs);
+    same_device(c.k, pages);
+    same_device(c.k, starts);
+    const c10::DeviceGuard guard(c.k.device());
+    const at::ScalarType type = out_type(a[7], a[8], "dtype");
+    at::Tensor out[2];
+    const char *names[2] = {"k_out", "v_out"};
+    for (int i = 0; i < 2; ++i) {
+      if (a[8 + i] == Py_None) {
+        out[i] = at::empty({tokens, c.heads, c.dim}, c.k.options().dtype(type));
+      } else {
+        out[i] = whole(a[8 + i], type, names[i]);
+        if (!has_shape(out[i], {tokens, c.heads, c.dim})) value_error("%s has the wrong shape", names[i]);
+        same_device(c.k, out[i]);
+      }
+    }
+    const int code = type_code(out[0], "dtype", true);
+    void *stream = stream_of(a[10], c.k);
+    auto bytes = [](const at::Tensor &t) { return static_cast<const uint8_t *>(t.data_ptr()); };
+    check(call([&] {
+      return lqmm_kv_read_f8(bytes(c.k), bytes(c.v), bytes(ks), bytes(vs),
+                             static_cast<const int32_t *>(pages.data_ptr()), pages.size(1),
+                             static_cast<const int32_t *>(starts.data_ptr()), out[0].data_ptr(),
+                             out[1].data_ptr(), code, tokens, pages.size(0), c.heads, c.dim, c.page_size,
+                             c.pages, stream);
+    }));
+    return both_of(out[0], out[1]);
+  });
+}
+
+// Attention over 16-bit caches, or over 8-bit ones with their scales. a: the
+// arguments of lqmm_attn_prefix in order.
+PyObject *attention(PyObject *const *a, bool f8, PyObject *k_scales, PyObject *v_scales) {
   return guarded([&]() -> PyObject * {
     const at::Tensor &q = tensor(a[0], "q");
-    const Caches c = caches(a[1], a[2]);
+    const Caches c = caches(a[1], a[2], f8);
     if (q.dim() != 3) value_error("%s must be (tokens, n_q_heads, head_dim)", "q");
     const int64_t tokens = q.size(0), heads = q.size(1);
     const int64_t ldq = row_stride(q, heads, c.dim, "q");
-    if (q.scalar_type() != c.k.scalar_type()) type_error("%s must have the caches' element type", "q");
+    if (!f8 && q.scalar_type() != c.k.scalar_type())
+      type_error("%s must have the caches' element type", "q");
+    const int type = f8 ? type_code(q, "q", false) : c.type;
+    const uint8_t *ks = nullptr, *vs = nullptr;
+    if (f8) {
+      const at::Tensor &kt = scale_bytes(k_scales, {c.pages, c.heads, c.page_size}, "k_scales");
+      const at::Tensor &vt = scale_bytes(v_scales, {c.pages, c.heads, c.page_size}, "v_scales");
+      same_device(q, kt);
+      same_device(q, vt);
+      ks = static_cast<const uint8_t *>(kt.data_ptr());
+      vs = static_cast<const uint8_t *>(vt.data_ptr());
+    }
     const at::Tensor &pages = whole(a[3], at::kInt, "pages");
     const at::Tensor &lens = whole(a[4], at::kInt, "seq_lens");
     if (pages.dim() != 2 || lens.dim() != 1 || pages.size(0) != lens.size(0))
@@ -325,8 +473,8 @@ PyObject *attn_prefix(PyObject *, PyObject *const *a, Py_ssize_t n) {
       ws = w.data_ptr();
       ws_bytes = (size_t)w.numel();
     } else {
-      const size_t need = lqmm_attn_prefix_workspace_bytes(prefix_len, max_pages, max_q, tokens, batch,
-                                                           heads, c.heads, c.dim, c.page_size);
+      const size_t need = (f8 ? lqmm_attn_prefix_f8_workspace_bytes : lqmm_attn_prefix_workspace_bytes)(
+          prefix_len, max_pages, max_q, tokens, batch, heads, c.heads, c.dim, c.page_size);
       // Its own workspace for every call, from the allocator's memory of the
       // stream it runs on: freed behind the launches, it is handed out again in
       // stream order, to whatever thread, and a graph under capture has its own.
@@ -346,7 +494,14 @@ PyObject *attn_prefix(PyObject *, PyObject *const *a, Py_ssize_t n) {
     }
     float *lse_p = lse.defined() ? static_cast<float *>(lse.data_ptr()) : nullptr;
     check(call([&] {
-      return lqmm_attn_prefix(q.data_ptr(), ldq, c.k.data_ptr(), c.v.data_ptr(), c.type, prefix,
+      if (f8)
+        return lqmm_attn_prefix_f8(q.data_ptr(), ldq, static_cast<const uint8_t *>(c.k.data_ptr()),
+                                   static_cast<const uint8_t *>(c.v.data_ptr()), ks, vs, type, prefix,
+                                   prefix_len, static_cast<const int32_t *>(pages.data_ptr()), max_pages,
+                                   static_cast<const int32_t *>(lens.data_ptr()), start, max_q,
+                                   out.data_ptr(), lse_p, (float)scale, tokens, batch, heads, c.heads,
+                                   c.dim, c.page_size, c.pages, ws, ws_bytes, stream);
+      return lqmm_attn_prefix(q.data_ptr(), ldq, c.k.data_ptr(), c.v.data_ptr(), type, prefix,
                               prefix_len, static_cast<const int32_t *>(pages.data_ptr()), max_pages,
                               static_cast<const int32_t *>(lens.data_ptr()), start, max_q,
                               out.data_ptr(), lse_p, (float)scale, tokens, batch, heads, c.heads,
@@ -360,6 +515,18 @@ PyObject *attn_prefix(PyObject *, PyObject *const *a, Py_ssize_t n) {
     Py_XDECREF(l);
     return both;
   });
+}
+
+PyObject *attn_prefix(PyObject *, PyObject *const *a, Py_ssize_t n) {
+  if (!arity(n, 15)) return nullptr;
+  return attention(a, false, nullptr, nullptr);
+}
+
+PyObject *attn_prefix_f8(PyObject *, PyObject *const *a, Py_ssize_t n) {
+  if (!arity(n, 17)) return nullptr;
+  PyObject *plain[15] = {a[0], a[1], a[2]};
+  for (int i = 3; i < 15; ++i) plain[i] = a[i + 2];
+  return attention(plain, true, a[3], a[4]);
 }
 
 // A 2-D contiguous device tensor of e4m3 codes (float8_e4m3fn or raw bytes).
@@ -452,6 +619,81 @@ PyObject *gemm_f8b128(PyObject *, PyObject *const *a, Py_ssize_t n) {
   });
 }
 
+// A 2-D contiguous device tensor of pairs of e2m1 codes.
+const at::Tensor &codes4(PyObject *o, const char *name) {
+  const at::Tensor &t = tensor(o, name);
+  if (t.scalar_type() != at::kByte && t.scalar_type() != at::kFloat4_e2m1fn_x2)
+    type_error("%s must be a uint8 (or float4_e2m1fn_x2) torch.Tensor", name);
+  whole(o, t.scalar_type(), name);
+  if (t.dim() != 2) value_error("%s must be 2-D", name);
+  return t;
+}
+
+PyObject *quant_mxfp4(PyObject *, PyObject *const *a, Py_ssize_t n) {
+  if (!arity(n, 4)) return nullptr;
+  return guarded([&]() -> PyObject * {
+    const at::Tensor &x = on_device(tensor(a[0], "X"), "X");
+    if (x.dim() != 2) value_error("%s must be (M, K)", "X");
+    const int64_t M = x.size(0), K = x.size(1);
+    if (K % 32 != 0) value_error("K of %s must be a multiple of 32", "X");
+    if (K > 1 && x.stride(1) != 1) value_error("the rows of %s must be contiguous", "X");
+    const int type = type_code(x, "X", true);
+    const c10::DeviceGuard guard(x.device());
+    at::Tensor out, scales;
+    if (a[1] == Py_None) {
+      out = at::empty({M, K / 2}, x.options().dtype(at::kByte));
+    } else {
+      out = codes4(a[1], "out");
+      if (!has_shape(out, {M, K / 2})) value_error("%s has the wrong shape", "out");
+      same_device(x, out);
+    }
+    if (a[2] == Py_None) {
+      scales = at::empty({M, K / 32}, x.options().dtype(at::kFloat8_e8m0fnu));
+    } else {
+      scales = scale_bytes(a[2], {M, K / 32}, "scales");
+      same_device(x, scales);
+    }
+    void *stream = stream_of(a[3], x);
+    check(call([&] {
+      return lqmm_quant_mxfp4(x.data_ptr(), type, M > 1 ? x.stride(0) : K,
+                              static_cast<uint8_t *>(out.data_ptr()),
+                              static_cast<uint8_t *>(scales.data_ptr()), M, K, stream);
+    }));
+    return both_of(out, scales);
+  });
+}
+
+PyObject *gemm_mxfp4(PyObject *, PyObject *const *a, Py_ssize_t n) {
+  if (!arity(n, 7)) return nullptr;
+  return guarded([&]() -> PyObject * {
+    const at::Tensor &w = codes4(a[0], "W"), &x = codes4(a[2], "Xq");
+    const int64_t N = w.size(0), K = 2 * w.size(1), M = x.size(0);
+    if (2 * x.size(1) != K) value_error("%s and Xq differ in K", "W");
+    const at::Tensor &ws = scale_bytes(a[1], {N, K / 32}, "wscale");
+    const at::Tensor &xs = scale_bytes(a[3], {M, K / 32}, "xscale");
+    same_device(w, ws);
+    same_device(w, x);
+    same_device(w, xs);
+    const c10::DeviceGuard guard(w.device());
+    const at::ScalarType type = out_type(a[5], a[4], "out_dtype");
+    at::Tensor out;
+    if (a[4] == Py_None) {
+      out = at::empty({M, N}, w.options().dtype(type));
+    } else {
+      out = whole(a[4], type, "out");
+      if (!has_shape(out, {M, N})) value_error("%s has the wrong shape", "out");
+      same_device(w, out);
+    }
+    const int code = type_code(out, "out", true);
+    void *stream = stream_of(a[6], w);
+    auto bytes = [](const at::Tensor &t) { return static_cast<const uint8_t *>(t.data_ptr()); };
+    check(call([&] {
+      return lqmm_gemm_mxfp4(bytes(w), bytes(ws), bytes(x), bytes(xs), out.data_ptr(), code, M, N, K, stream);
+    }));
+    return THPVariable_Wrap(out);
+  });
+}
+
 PyObject *setup(PyObject *, PyObject *const *a, Py_ssize_t n) {
   if (!arity(n, 3)) return nullptr;
   PyObject **to[] = {&g_raise_status, &g_raw_stream, &g_workspace_on};
@@ -470,6 +712,11 @@ PyMethodDef kMethods[] = {
     {"attn_prefix", FASTCALL(attn_prefix), nullptr},
     {"quant_f8b128", FASTCALL(quant_f8b128), nullptr},
     {"gemm_f8b128", FASTCALL(gemm_f8b128), nullptr},
+    {"kv_append_norm", FASTCALL(kv_append_norm), nullptr},
+    {"kv_read_f8", FASTCALL(kv_read_f8), nullptr},
+    {"attn_prefix_f8", FASTCALL(attn_prefix_f8), nullptr},
+    {"quant_mxfp4", FASTCALL(quant_mxfp4), nullptr},
+    {"gemm_mxfp4", FASTCALL(gemm_mxfp4), nullptr},
     {nullptr, nullptr, 0, nullptr}};
 PyModuleDef kModule = {PyModuleDef_HEAD_INIT, "_serve", "Native calls of the serving operators.", -1,
                        kMethods, nullptr, nullptr, nullptr, nullptr};

@@ -368,6 +368,102 @@ lqmm_status lqmm_gemm_f8b128(const uint8_t *W, const float *wscale, const uint8_
 lqmm_status lqmm_quant_f8b128(const void *X, int x_type, int64_t ldx, uint8_t *Xq, float *xscale,
                               int64_t M, int64_t K, void *stream);
 
+/*
+ * ---- serving operators in fewer bits -----------------------------------------
+ *
+ * The 8-bit paged cache. Each token's vector of one head is head_dim e4m3 codes
+ * (finite-only, largest value 448; 0x7F and 0xFF are NaN) and a power of two,
+ * held as one byte, its exponent + 127:
+ *   k_cache  [num_pages][n_kv_heads][page_size][head_dim]           codes
+ *   v_cache  [num_pages][n_kv_heads][page_size / 8][head_dim][8]    codes
+ *   k_scales, v_scales  [num_pages][n_kv_heads][page_size]          bytes
+ * A vector x is held with the least exponent e for which max |x| <= 448 * 2^e,
+ * at least -60 (smaller values lose digits) and at most 60, or 7 in a call whose
+ * type is fp16 (larger values are held as the largest code); its codes are x *
+ * 2^-e to nearest even. An infinity or NaN is held as NaN and does not count for
+ * e. Reading, bytes 1 to 253 are scales; what 0, 254 and 255 stand for is left
+ * open, for the rows that see such a key.
+ */
+
+/*
+ * lqmm_kv_append with a norm of each head of q and k before the rotation,
+ *   y = x / sqrt(mean(x^2) + eps) * weight,
+ * into a 16-bit cache (NULL scales; of `type`) or an 8-bit one (both scales).
+ * q_norm, k_norm: head_dim fp32 weights each, the same for every head; NULL: no
+ * norm. eps >= 0. q_out is of `type` (fp16 or bf16) with either cache.
+ * Everything else is as for lqmm_kv_append. No other token's codes or scales
+ * are touched.
+ */
+lqmm_status lqmm_kv_append_norm(const void *q, const void *k, const void *v, int in_type,
+                                int64_t ldq, int64_t ldk, int64_t ldv, const int32_t *positions,
+                                const int64_t *slots, const uint64_t *rope_turns,
+                                int64_t rotary_dim, int interleaved, const float *q_norm,
+                                const float *k_norm, float eps, void *q_out, void *k_cache,
+                                void *v_cache, uint8_t *k_scales, uint8_t *v_scales, int type,
+                                int64_t tokens, int64_t n_q_heads, int64_t n_kv_heads,
+                                int64_t head_dim, int64_t page_size, int64_t num_pages,
+                                void *stream);
+
+/*
+ * The 8-bit cache back to dense rows, for handing a conversation on: row
+ * starts[b] + j of k_out and v_out (tokens x n_kv_heads x head_dim of `type`:
+ * fp32, fp16 or bf16) is token j of sequence b's pages[b][0 .. max_pages), each
+ * value rounded once (exact in fp32 and bf16; fp16 has steps of 2^-24 and values
+ * past 65504 are infinite). starts: batch + 1 int32, not decreasing, on the
+ * device. Rows before starts[0] and from starts[batch] on are zeros, and so are
+ * tokens past the page table; a page number outside the cache reads page 0.
+ */
+lqmm_status lqmm_kv_read_f8(const uint8_t *k_cache, const uint8_t *v_cache, const uint8_t *k_scales,
+                            const uint8_t *v_scales, const int32_t *pages, int64_t max_pages,
+                            const int32_t *starts, void *k_out, void *v_out, int type,
+                            int64_t tokens, int64_t batch, int64_t n_kv_heads, int64_t head_dim,
+                            int64_t page_size, int64_t num_pages, void *stream);
+
+/*
+ * lqmm_attn_prefix over the 8-bit cache; `type` (fp16 or bf16) is that of q and
+ * out. A key enters the products as its value rounded to `type` (exact but for
+ * fp16 values below 2^-14, in steps of 2^-24); V's codes enter as they are, and
+ * their scales count in the softmax's weights before these are rounded to
+ * `type`. The rest is as for lqmm_attn_prefix, a NaN code being a NaN value.
+ */
+lqmm_status lqmm_attn_prefix_f8(const void *q, int64_t ldq, const uint8_t *k_cache,
+                                const uint8_t *v_cache, const uint8_t *k_scales,
+                                const uint8_t *v_scales, int type, const int32_t *prefix_pages,
+                                int64_t prefix_len, const int32_t *pages, int64_t max_pages,
+                                const int32_t *seq_lens, const int32_t *q_start, int64_t max_q,
+                                void *out, float *lse, float scale, int64_t tokens, int64_t batch,
+                                int64_t n_q_heads, int64_t n_kv_heads, int64_t head_dim,
+                                int64_t page_size, int64_t num_pages, void *workspace,
+                                size_t workspace_bytes, void *stream);
+/* Bytes that call needs for these sizes (as lqmm_attn_prefix_workspace_bytes). */
+size_t lqmm_attn_prefix_f8_workspace_bytes(int64_t prefix_len, int64_t max_pages, int64_t max_q,
+                                           int64_t tokens, int64_t batch, int64_t n_q_heads,
+                                           int64_t n_kv_heads, int64_t head_dim, int64_t page_size);
+
+/*
+ * Microscaled 4-bit floats (OCP Microscaling Formats v1.0, MXFP4). A row of K
+ * values (K % 32 == 0) is K / 2 bytes of e2m1 codes, two a byte, the first in
+ * the low half, and K / 32 scale bytes, one for each block of 32. A code is a
+ * sign (bit 3) and 0, 0.5, 1, 1.5, 2, 3, 4, 6; a scale byte s is 2^(s - 127), 255
+ * NaN. Scale bytes need no alignment.
+ *
+ * lqmm_quant_mxfp4: X (M x K of x_type: fp32, fp16, bf16; row stride ldx) to
+ * codes and scales: the scale is 2^(floor(log2 max |x|) - 2), at least 2^-127,
+ * and the codes are x / scale to nearest even, saturated at 6. A block with an
+ * infinity or NaN gets the scale NaN and codes 0.
+ */
+lqmm_status lqmm_quant_mxfp4(const void *X, int x_type, int64_t ldx, uint8_t *Xq, uint8_t *xscale,
+                             int64_t M, int64_t K, void *stream);
+/*
+ * Y = X * W^T of two such matrices, W: N x K and X: M x K, with fp32 sums,
+ * rounded once to y_type (fp32, fp16 or bf16). Y is M x N; any M and N, K a
+ * multiple of 32 and < LQMM_GEMM_MAX_K. A block whose scale is NaN makes its
+ * row's (or column's) outputs NaN.
+ */
+lqmm_status lqmm_gemm_mxfp4(const uint8_t *W, const uint8_t *wscale, const uint8_t *Xq,
+                            const uint8_t *xscale, void *Y, int y_type, int64_t M, int64_t N,
+                            int64_t K, void *stream);
+
 /* Workspace the GEMV calls of these sizes can use, in bytes (0 = none):
  * enough for every GEMV entry point on any device. */
 size_t lqmm_gemv_workspace_bytes(int64_t N, int64_t K, int64_t batch);
