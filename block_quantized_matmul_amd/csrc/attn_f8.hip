@@ -404,11 +404,527 @@ attn_f8_rows16_kernel(AttnPrefixF8 a, uint32_t item0) {
     rows16_body<T, D, kThreads / 64>(a, it, sm);
 }
 
+// ---- many rows -----------------------------------------------------------------
+// As in attn_prefix.hip: 32 R rows a wave, all waves of a workgroup take the same
+// keys from LDS tiles of 16-bit operands. Here the codes come through registers
+// and are converted once for all waves on their way into LDS (K with its scales;
+// V's go beside it, as the exponents and powers that logits and sums take).
+//
+// A running maximum that grows by no more than kSlack (log2) is left where it
+// is: O is rescaled when a row needs it, not at every step.
+constexpr float kSlack = 8.0f;
+// Weights are at most 2^(kSlack + kWideShift): 2^kShift.
+template <class T>
+constexpr float kWideShift = kShift<T> - kSlack;
+
+// Waves of a SIMD that the wide kernel's registers leave room for.
+constexpr int wide_waves(int d, int nw, int r) {
+  return r > 1 ? (d == 64 ? 2 : 1) : d <= 128 && nw == 8 ? 2 : 1;
+}
+
+template <int D>
+struct Wide {
+  static constexpr int kKeys = D <= 128 ? 64 : 32;  // keys of a tile
+  static constexpr int kHalf = kKeys * D * 2;       // bytes of a tile's K (and V)
+  // a round is two tiles between barriers: K of it and of the tile after, V of
+  // it, and the next round's two tiles of each on their way
+  static constexpr int kStagesK = 5, kStagesV = 4;
+  // V's exponents and their inverse powers, of as many tiles as K
+  static constexpr int kScales = 2 * kKeys * 4;
+  static constexpr int kLds = (kStagesK + kStagesV) * kHalf + kStagesK * kScales;
+};
+
+// The rows of a wave again, if its mask's edge asks for it (whether it did). Item
+// and arguments are read once more, so that nothing of them is held in registers
+// through the keys' loop for this.
+template <class T, int D>
+__device__ __forceinline__ bool wave_again(uint32_t item0, int rows_per_block, int from, int n) {
+  uint64_t args = (uint64_t)__builtin_amdgcn_kernarg_segment_ptr();
+  uint32_t block = blockIdx.x;
+  asm volatile("" : "+s"(args), "+s"(block));
+  const AttnPrefixF8 &a = *reinterpret_cast<const AttnPrefixF8 *>(args);  // the kernel's first argument
+  Item it;
+  if (!find_item(a, item0 + spread(block, gridDim.x), rows_per_block, it)) return false;
+  const int row0 = it.row0 + from;
+  if (row0 >= it.rows || !edge_has_nan<D>(a, it, it.past + it.per_token * (row0 / a.group))) return false;
+  const int end = row0 + n < it.rows ? row0 + n : it.rows;
+  for (int i = row0; i < end; ++i) row_alone<T, D>(a, it, i);
+  return true;
+}
+
+template <class T, int D, int NW, int R>
+__device__ __forceinline__ void wide_body(const AttnPrefixF8 &a, const Item &it, uint32_t item0,
+                                          uint8_t *smem) {
+  typedef typename T::elem elem;
+  typedef typename T::vec8 vec8;
+  typedef Wide<D> C;
+  constexpr int KT = C::kKeys;
+  constexpr int kQ = D / 16;                     // k-steps of a logit tile
+  constexpr int kDT = D / 32;                    // 32-wide tiles of O
+  constexpr int kGroups = KT / 8 / NW;           // eight-key groups that a wave brings
+  constexpr int kUnits = kGroups * D / 2;        // 16-byte units of their K, and of their V
+  constexpr int kLoads = (kUnits + 63) / 64;     // of a lane
+  static_assert(KT % (8 * NW) == 0 && kGroups <= 2, "whole groups");
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int l32 = lane & 31, h = lane >> 5;
+  const int G = a.group;
+  const int lg = a.page_log2, pmask = (1 << lg) - 1;
+  const bool direct = a.prefix_parts + a.suffix_parts == 1;
+
+  // This wave's rows, in R tiles of 32.
+  const int row0 = it.row0 + 32 * R * wave;
+  int limit[R];  // keys below it are seen
+  vec8 q[R][kQ];
+#pragma unroll
+  for (int w = 0; w < R; ++w) {
+    const int row = row0 + 32 * w + l32;
+    const bool live = row < it.rows;
+    const int tok = live ? row / G : 0;
+    const int hq = it.h * G + (live ? row % G : 0);
+    limit[w] = it.past + it.per_token * tok;
+    const elem *src = static_cast<const elem *>(a.q) + (it.tok0 + tok) * a.ldq + (int64_t)hq * D + 8 * h;
+#pragma unroll
+    for (int i = 0; i < kQ; ++i) {
+      const u32x4 x = *reinterpret_cast<const u32x4 *>(src + 16 * i);
+      q[w][i] = __builtin_bit_cast(vec8, x ^ a.q_sign);
+    }
+  }
+  const int all_see = it.past + it.per_token * (row0 < it.rows ? row0 / G : 0);
+
+  // Loads. A group of eight keys is 8 D bytes in one piece, of K and of V, at
+  // the same offset. A wave brings kGroups groups of a tile, whose page numbers
+  // are the same in all lanes (scalar loads). Unit u of a group is 16 dimensions
+  // of key u / (D / 16), and of V dimensions 2 u and 2 u + 1 of the eight keys. In
+  // LDS, row `key` of K has its 16-byte chunks exchanged by `swz(key)`, so that the
+  // eight rows of one read phase (keys 0-3 and 8-11, or 4-7 and 12-15) lie in
+  // different banks; V is as in memory.
+  const uint8_t *kc = static_cast<const uint8_t *>(a.k_cache);
+  const uint8_t *vc = static_cast<const uint8_t *>(a.v_cache);
+  auto swz = [](int key) {
+    return D == 96 ? (key & 3) : (key & 3) + 4 * (key >> 3 & 1);
+  };
+  const int last_group = (it.c1 - 1) & ~7;
+  typedef const __attribute__((address_space(4))) int32_t *constant_ptr;
+  const constant_ptr pages = (constant_ptr)(uintptr_t)it.pages;
+  auto first_vector = [&](int j0, int i) {  // of the wave's group i of the tile at key j0
+    int j = j0 + 8 * (kGroups * wave + i);
+    j = j < last_group ? j : last_group;
+    const int32_t p = pages[j >> lg];
+    const int64_t page = (uint32_t)p < (uint32_t)a.num_pages ? p : 0;
+    return ((page * a.n_kv_heads + it.h) << lg) + (j & pmask);
+  };
+  struct Codes {  // of a tile, on their way
+    u32x4 c[kLoads];
+    uint32_t s[kLoads], v;  // (K's scales, and V's beside them: logits take both)
+  };
+  auto unit_of = [&](int i, int &group, int &u) {
+    const int v = 64 * i + lane;
+    group = kGroups > 1 ? v / (D / 2) : 0;
+    u = kGroups > 1 ? v % (D / 2) : v;
+    return kUnits % 64 == 0 || v < kUnits;
+  };
+  auto load_k = [&](Codes &x, int j0) {
+    int64_t vec[kGroups];
+#pragma unroll
+    for (int g = 0; g < kGroups; ++g) vec[g] = first_vector(j0, g);
+#pragma unroll
+    for (int i = 0; i < kLoads; ++i) {
+      int g, u;
+      if (!unit_of(i, g, u)) continue;
+      const int64_t at = kGroups > 1 && g ? vec[kGroups - 1] : vec[0];
+      x.c[i] = *reinterpret_cast<const u32x4 *>(kc + at * D + 16 * u);
+      x.s[i] = a.k_scales[at + u / (D / 16)];
+    }
+    // V's scales: lane i of the wave has that of key i of its groups
+    const int64_t at = kGroups > 1 && (lane & 8) ? vec[kGroups - 1] : vec[0];
+    x.v = a.v_scales[at + (lane & 7)];
+  };
+  auto load_v = [&](Codes &x, int j0) {
+    int64_t vec[kGroups];
+#pragma unroll
+    for (int g = 0; g < kGroups; ++g) vec[g] = first_vector(j0, g);
+#pragma unroll
+    for (int i = 0; i < kLoads; ++i) {
+      int g, u;
+      if (!unit_of(i, g, u)) continue;
+      const int64_t at = kGroups > 1 && g ? vec[kGroups - 1] : vec[0];
+      x.c[i] = *reinterpret_cast<const u32x4 *>(vc + at * D + 16 * u);
+    }
+  };
+  uint8_t *const vsmem = smem + C::kStagesK * C::kHalf;
+  uint8_t *const ssmem = vsmem + C::kStagesV * C::kHalf;
+  auto k_stage = [&](int tile) { return smem + tile % C::kStagesK * C::kHalf; };
+  auto v_stage = [&](int tile) { return vsmem + tile % C::kStagesV * C::kHalf; };
+  // exponents [KT], and inverse powers [KT]
+  auto s_stage = [&](int tile) { return reinterpret_cast<float *>(ssmem + tile % C::kStagesK * C::kScales); };
+  auto store_k = [&](const Codes &x, int tile) {
+    uint8_t *st = k_stage(tile);
+#pragma unroll
+    for (int i = 0; i < kLoads; ++i) {
+      int g, u;
+      if (!unit_of(i, g, u)) continue;
+      const int key = 8 * (kGroups * wave + g) + u / (D / 16), chunk = 2 * (u % (D / 16));
+      const float f = scale_of(x.s[i]);
+      uint8_t *to = st + key * (2 * D);
+      *reinterpret_cast<vec8 *>(to + 16 * (chunk ^ swz(key))) = values8<T>(u32x2{x.c[i][0], x.c[i][1]}, f);
+      *reinterpret_cast<vec8 *>(to + 16 * ((chunk + 1) ^ swz(key))) = values8<T>(u32x2{x.c[i][2], x.c[i][3]}, f);
+    }
+    if (lane < 8 * kGroups) {
+      float *sc = s_stage(tile) + 8 * kGroups * wave + lane;
+      const uint32_t b = x.v < 253u ? x.v : 253u;  // (of a key that is not seen anything)
+      sc[0] = (float)((int)b - 127);
+      sc[KT] = scale_inverse(b);
+    }
+  };
+  auto store_v = [&](const Codes &x, int tile, int j0) {
+    uint8_t *st = v_stage(tile);
+#pragma unroll
+    for (int i = 0; i < kLoads; ++i) {
+      int g, u;
+      if (!unit_of(i, g, u)) continue;
+      // what lies behind the last key may be anything, and 0 * NaN is NaN
+      const int group = kGroups * wave + g, valid = it.c1 - (j0 + 8 * group);
+      const uint32_t lo = valid >= 4 ? ~0u : valid <= 0 ? 0u : ~0u >> (32 - 8 * valid);
+      const uint32_t hi = valid >= 8 ? ~0u : valid <= 4 ? 0u : ~0u >> (64 - 8 * valid);
+      vec8 *to = reinterpret_cast<vec8 *>(st + (group * D + 2 * u) * 16);
+      to[0] = values8<T>(u32x2{x.c[i][0] & lo, x.c[i][1] & hi}, 1.0f);
+      to[1] = values8<T>(u32x2{x.c[i][2] & lo, x.c[i][3] & hi}, 1.0f);
+    }
+  };
+
+  float16_t o[R][kDT];
+  float m[R], l[R], top[R];
+  float ref[R];  // m - kWideShift<T>, finite
+#pragma unroll
+  for (int w = 0; w < R; ++w) {
+    m[w] = top[w] = -INFINITY;
+    l[w] = ref[w] = 0.f;
+#pragma unroll
+    for (int i = 0; i < kDT; ++i)
+#pragma unroll
+      for (int r = 0; r < 16; ++r) o[w][i][r] = 0.f;
+  }
+
+  // A step is 32 keys. S^T of a step: row m is key 16 (m / 16) + 8 (m / 4 % 2)
+  // + 4 (m / 8 % 2) + m % 4, which leaves the weights of the step's 16-key
+  // halves as the B operands of O^T = V^T P^T.
+  const int key_of_lane = (l32 & 16) + 8 * (l32 >> 2 & 1) + 4 * (l32 >> 3 & 1) + (l32 & 3);
+  constexpr int kM = kQ / 2;  // logit products of half a step
+  static_assert(kM == kDT, "as many products of V in half a step");
+  auto k_operand = [&](const uint8_t *ks, int sub, int i) {
+    const int key = 32 * sub + key_of_lane;
+    return *reinterpret_cast<const vec8 *>(ks + key * (2 * D) + 16 * ((2 * i + h) ^ swz(key)));
+  };
+  auto v_operand = [&](const uint8_t *vs, int half, int i) {  // 16 keys `half`, dimensions 32 i ..
+    return *reinterpret_cast<const vec8 *>(vs + ((2 * half + h) * D + 32 * i + l32) * 16);
+  };
+  typedef float16_t Logits[R];
+  auto mask = [&](int j0, Logits &s) {
+    asm volatile("");  // stays behind its branch: few steps need it
+#pragma unroll
+    for (int w = 0; w < R; ++w) {
+      const int seen = (limit[w] < it.c1 ? limit[w] : it.c1) - j0 - 8 * h;
+#pragma unroll
+      for (int r = 0; r < 16; ++r)
+        if (16 * (r >> 3) + (r & 7) >= seen) s[w][r] = -INFINITY;
+    }
+  };
+  const int plain_end = it.c1 < all_see ? it.c1 : all_see;  // steps up to here need no mask
+  // Half c of a step's keys: this lane's eight (exponents, or inverse powers at + KT).
+  auto eight = [&](const float *sc, int sub, int c, float (&x)[8]) {
+    const float4_t *p = reinterpret_cast<const float4_t *>(sc + 32 * sub + 16 * c + 8 * h);
+    const float4_t lo = p[0], hi = p[1];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) x[e] = lo[e], x[4 + e] = hi[e];
+  };
+
+  // One step: the weights of s (32 keys, V at vs + `sub`, scales sv) on the vector
+  // ALU beside the logits of the next 32 keys (from jn, K at kn + `nsub`; past the
+  // last key: of what is there, masked) on the matrix cores, then the products
+  // with V beside the next logits' scales (sn) and maximum. Each half reads the
+  // next one's operands from LDS, the last one those of K for the step after (K at
+  // ka + `asub`; one-step tiles read them at the step's start, behind the barrier).
+  constexpr bool kCarry = KT == 64;
+  vec8 k0[kM];
+  auto step = [&](const uint8_t *vs, const float *sv, int sub, const Logits &s, const uint8_t *kn,
+                  const float *sn, int nsub, int jn, Logits &next, const uint8_t *ka, int asub) {
+    bool grown = false;
+#pragma unroll
+    for (int w = 0; w < R; ++w) grown = grown || top[w] > m[w] + kSlack;
+    if (__any(grown)) {
+#pragma unroll
+      for (int w = 0; w < R; ++w) {
+        const float mn = fmaxf(m[w], top[w]);
+        const float to = (mn == -INFINITY ? 0.f : mn) - kWideShift<T>;
+        const float c = m[w] == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(ref[w] - to);
+        m[w] = mn;
+        ref[w] = to;
+        l[w] *= c;
+#pragma unroll
+        for (int i = 0; i < kDT; ++i)
+#pragma unroll
+          for (int r = 0; r < 16; ++r) o[w][i][r] *= c;
+      }
+    }
+    vec8 p[R][2], k1[kM], vf[2][kDT];
+    if constexpr (!kCarry) {
+#pragma unroll
+      for (int i = 0; i < kM; ++i) k0[i] = k_operand(kn, nsub, i);
+    }
+    __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+    for (int c = 0; c < 2; ++c) {
+      float back[8];
+      eight(sv + KT, sub, c, back);
+      if (c == 0) {
+#pragma unroll
+        for (int i = 0; i < kM; ++i) k1[i] = k_operand(kn, nsub, kM + i);
+      } else {
+#pragma unroll
+        for (int i = 0; i < kDT; ++i) vf[0][i] = v_operand(vs, 2 * sub, i);
+      }
+#pragma unroll
+      for (int i = 0; i < kM; ++i)
+#pragma unroll
+        for (int w = 0; w < R; ++w)
+          next[w] = T::mfma32(c == 0 ? k0[i] : k1[i], q[w][c * kM + i], c + i == 0 ? float16_t{} : next[w]);
+#pragma unroll
+      for (int w = 0; w < R; ++w) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const float x = __builtin_amdgcn_exp2f(s[w][8 * c + e] - ref[w]);
+          l[w] = fmaf(x, back[e], l[w]);
+          p[w][c][e] = (elem)x;
+        }
+        asm volatile("" : "+v"(p[w][c]));  // computed here, not after the mask's branch
+      }
+      // matrix and vector instructions in turn
+      __builtin_amdgcn_sched_group_barrier(0x100, kM + 2, 0);
+#pragma unroll
+      for (int i = 0; i < R * kM; ++i) {
+        __builtin_amdgcn_sched_group_barrier(0x8, 1, 0);
+        __builtin_amdgcn_sched_group_barrier(0x402, 28 / kM, 0);
+      }
+      __builtin_amdgcn_sched_barrier(0);
+    }
+    if (jn + 32 > plain_end) mask(jn, next);
+    float x[R];
+#pragma unroll
+    for (int w = 0; w < R; ++w) x[w] = -INFINITY;
+#pragma unroll
+    for (int c = 0; c < 2; ++c) {
+      float ex[8];
+      eight(sn, nsub, c, ex);
+      if (c == 0) {
+#pragma unroll
+        for (int i = 0; i < kDT; ++i) vf[1][i] = v_operand(vs, 2 * sub + 1, i);
+      } else if constexpr (kCarry) {
+#pragma unroll
+        for (int i = 0; i < kM; ++i) k0[i] = k_operand(ka, asub, i);
+      }
+#pragma unroll
+      for (int i = 0; i < kDT; ++i)
+#pragma unroll
+        for (int w = 0; w < R; ++w) o[w][i] = T::mfma32(vf[c][i], p[w][c], o[w][i]);
+#pragma unroll
+      for (int w = 0; w < R; ++w)
+#pragma unroll
+        for (int e = 0; e < 8; e += 2) {
+          const float y0 = fmaf(next[w][8 * c + e], a.scale_log2, ex[e]);
+          const float y1 = fmaf(next[w][8 * c + e + 1], a.scale_log2, ex[e + 1]);
+          next[w][8 * c + e] = y0, next[w][8 * c + e + 1] = y1;
+          x[w] = fmaxf(fmaxf(y0, y1), x[w]);
+        }
+      __builtin_amdgcn_sched_group_barrier(0x100, kDT + 2, 0);
+#pragma unroll
+      for (int i = 0; i < R * kDT; ++i) {
+        __builtin_amdgcn_sched_group_barrier(0x8, 1, 0);
+        __builtin_amdgcn_sched_group_barrier(0x2, 4, 0);
+      }
+      __builtin_amdgcn_sched_barrier(0);
+    }
+#pragma unroll
+    for (int w = 0; w < R; ++w) top[w] = max_over_halves(x[w]);
+  };
+
+  // K is used up to one tile before V: what goes out together is K of tile p + 1
+  // and V of tile p.
+  const int tiles = (it.c1 - it.c0 + KT - 1) / KT;
+  Logits s, s2;
+  Codes xk, xv;
+  auto load_pair = [&](int p) {
+    load_k(xk, it.c0 + (p + 1) * KT);
+    load_v(xv, it.c0 + p * KT);
+  };
+  auto store_pair = [&](int p) {
+    store_k(xk, p + 1);
+    store_v(xv, p, it.c0 + p * KT);
+  };
+  if (tiles > 0) {
+    load_k(xk, it.c0);
+    store_k(xk, 0);
+    load_pair(0);
+    store_pair(0);
+    load_pair(1);
+    if (tiles > 1) store_pair(1);
+    load_pair(2);
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < kQ; ++i) {
+      const vec8 k = k_operand(smem, 0, i);
+#pragma unroll
+      for (int w = 0; w < R; ++w) s[w] = T::mfma32(k, q[w][i], i == 0 ? float16_t{} : s[w]);
+    }
+    if (it.c0 + 32 > plain_end) mask(it.c0, s);
+#pragma unroll
+    for (int w = 0; w < R; ++w) {
+      float x = -INFINITY;
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        float ex[8];
+        eight(s_stage(0), 0, c, ex);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          s[w][8 * c + e] = fmaf(s[w][8 * c + e], a.scale_log2, ex[e]);
+          x = fmaxf(x, s[w][8 * c + e]);
+        }
+      }
+      top[w] = max_over_halves(x);
+    }
+    if constexpr (kCarry) {
+#pragma unroll
+      for (int i = 0; i < kM; ++i) k0[i] = k_operand(smem, 1, i);
+    }
+  }
+  for (int round = 0; round < tiles; round += 2) {
+    if (round) __syncthreads();
+#pragma unroll
+    for (int b = 0; b < 2; ++b) {
+      const int kt = round + b, j0 = it.c0 + kt * KT;
+      if (kt >= tiles) break;
+      const uint8_t *vs = v_stage(kt), *kn = k_stage(kt + 1);
+      const float *sv = s_stage(kt), *sn = s_stage(kt + 1);
+      if constexpr (KT == 64) {
+        step(vs, sv, 0, s, k_stage(kt), sv, 1, j0 + 32, s2, kn, 0);
+        step(vs, sv, 1, s2, kn, sn, 0, j0 + 64, s, kn, 1);
+      } else {
+        step(vs, sv, 0, s, kn, sn, 0, j0 + 32, s2, nullptr, 0);
+#pragma unroll
+        for (int w = 0; w < R; ++w) s[w] = s2[w];
+      }
+      // the pair of the tile two ahead, whose codes have come; the next one goes out
+      if (kt + 2 < tiles) {
+        store_pair(kt + 2);
+        load_pair(kt + 3);
+      }
+    }
+  }
+
+  // this lane's rows again: nothing of them is held through the loop
+  int lane_row = l32;
+  asm volatile("" : "+v"(lane_row));
+  bool live[R];
+  int64_t flat[R];  // (token, head)
+#pragma unroll
+  for (int w = 0; w < R; ++w) {
+    const int row = row0 + 32 * w + lane_row;
+    live[w] = row < it.rows;
+    const int tok = live[w] ? row / G : 0;
+    flat[w] = (it.tok0 + tok) * a.n_q_heads + it.h * G + (live[w] ? row % G : 0);
+  }
+  if (it.c1 > plain_end) {
+    bool bad = false;  // (of rows that are there)
+#pragma unroll
+    for (int w = 0; w < R; ++w)
+#pragma unroll
+      for (int i = 0; i < kDT; ++i)
+#pragma unroll
+        for (int r = 0; r < 16; ++r) bad = bad || (live[w] && o[w][i][r] != o[w][i][r]);
+    if (__any(bad) && wave_again<T, D>(item0, 32 * R * NW, 32 * R * wave, 32 * R)) return;
+  }
+
+  const int64_t nrows = a.tokens * a.n_q_heads;
+#pragma unroll
+  for (int w = 0; w < R; ++w) {
+    const float sum = sum_over_halves(l[w]);
+    if (!live[w]) continue;
+    if (direct) {
+      typedef elem vec4 __attribute__((ext_vector_type(4)));
+      const float inv = sum == 0.f ? 0.f : 1.0f / sum;
+      elem *dst = static_cast<elem *>(a.out) + flat[w] * D + 4 * h;
+#pragma unroll
+      for (int i = 0; i < kDT; ++i)
+#pragma unroll
+        for (int r = 0; r < 16; r += 4)
+          *reinterpret_cast<vec4 *>(dst + 32 * i + 2 * r) =
+              vec4{(elem)(o[w][i][r] * inv), (elem)(o[w][i][r + 1] * inv),
+                   (elem)(o[w][i][r + 2] * inv), (elem)(o[w][i][r + 3] * inv)};
+      if (h == 0 && a.lse) a.lse[flat[w]] = lse_of(m[w] - kWideShift<T>, sum);
+    } else {
+      float *dst = a.part_o + (it.part * nrows + flat[w]) * D + 4 * h;
+#pragma unroll
+      for (int i = 0; i < kDT; ++i)
+#pragma unroll
+        for (int r = 0; r < 16; r += 4)
+          *reinterpret_cast<float4_t *>(dst + 32 * i + 2 * r) =
+              float4_t{o[w][i][r], o[w][i][r + 1], o[w][i][r + 2], o[w][i][r + 3]};
+      if (h == 0) a.part_ml[it.part * nrows + flat[w]] = make_float2(m[w] - kWideShift<T>, sum);
+    }
+  }
+}
+
+template <class T, int D, int NW, int R>
+__global__ void __launch_bounds__(64 * NW, wide_waves(D, NW, R))
+attn_f8_wide_kernel(AttnPrefixF8 a, uint32_t item0) {
+  extern __shared__ __attribute__((aligned(16))) uint8_t smem[];
+  Item it;
+  const uint32_t idx = item0 + spread(blockIdx.x, gridDim.x);
+  rows_of_no_sequence<T, D>(a, idx, 64 * NW);
+  if (find_item(a, idx, 32 * R * NW, it))
+    wide_body<T, D, NW, R>(a, it, item0, smem);
+}
+
+template <class T, int D, int NW, int R>
+hipError_t launch_wide(const AttnPrefixF8 &a, int64_t item0, int64_t items, hipStream_t stream) {
+  constexpr auto kern = attn_f8_wide_kernel<T, D, NW, R>;
+  const hipError_t e = ensure_max_lds<kern>(Wide<D>::kLds);
+  if (e != hipSuccess) return e;
+  return launch_in_pieces(items, 64 * NW, [&](uint32_t first, unsigned n) {
+    hipLaunchKernelGGL(kern, dim3(n), dim3(64 * NW), Wide<D>::kLds, stream, a, (uint32_t)item0 + first);
+  });
+}
+
+// Workgroups of 256 rows are eight waves of 32, or four of 64, as in
+// attn_prefix.hip.
+template <class T, int D>
+hipError_t launch_items(const AttnPrefixF8 &a, int wide, int64_t item0, int64_t items,
+                        hipStream_t stream) {
+  if (items == 0) return hipSuccess;
+  if (wide == 2) {
+    if constexpr (D == 128) return launch_wide<T, D, 8, 1>(a, item0, items, stream);
+    if constexpr (D < 128) return launch_wide<T, D, 4, 2>(a, item0, items, stream);
+    return hipErrorInvalidValue;
+  }
+  if (wide == 1) return launch_wide<T, D, 4, 1>(a, item0, items, stream);
+  return launch_in_pieces(items, kThreads, [&](uint32_t first, unsigned n) {
+    hipLaunchKernelGGL((attn_f8_rows16_kernel<T, D>), dim3(n), dim3(kThreads), 0, stream, a,
+                       (uint32_t)item0 + first);
+  });
+}
+
+// The prefix's and the suffixes' items are launched together when they are of
+// one kind.
 template <class T, int D>
 hipError_t launch(const AttnPrefixF8 &a, hipStream_t stream) {
-  hipError_t e = launch_in_pieces(a.prefix_items + a.suffix_items, kThreads, [&](uint32_t first, unsigned n) {
-    hipLaunchKernelGGL((attn_f8_rows16_kernel<T, D>), dim3(n), dim3(kThreads), 0, stream, a, first);
-  });
+  hipError_t e;
+  if (a.prefix_wide == a.suffix_wide || a.prefix_items == 0) {
+    e = launch_items<T, D>(a, a.suffix_wide, 0, a.prefix_items + a.suffix_items, stream);
+  } else {
+    e = launch_items<T, D>(a, a.prefix_wide, 0, a.prefix_items, stream);
+    if (e != hipSuccess) return e;
+    e = launch_items<T, D>(a, a.suffix_wide, a.prefix_items, a.suffix_items, stream);
+  }
   if (e != hipSuccess || a.prefix_parts + a.suffix_parts == 1) return e;
   constexpr int kRowsPerBlock = kThreads / (D / 4);
   const int64_t nrows = a.tokens * a.n_q_heads;
@@ -434,27 +950,57 @@ hipError_t launch_dim(const AttnPrefixF8 &a, hipStream_t stream) {
 // Splits the keys so that the launch fills the chip. A chunk is a multiple of
 // 128 keys and at most kAttnMaxChunk.
 void attn_f8_plan(AttnPrefixF8 &a, int64_t max_suffix, int num_cus) {
-  auto chunk_of = [&](int64_t keys, int64_t blocks) {
+  // Rows of a work item: 16 while reading the cache is the cost, else 128 or
+  // 256 (wide 1, 2). Measured, a prefix of 16001 keys, 8 key heads, fp16 (us;
+  // 16-row / 128 / 256): 128 dimensions, 32 rows 29.5 / 33.6 / 35.3, 48 rows
+  // 37.3 / 34.5 / 36.2, 128 rows 81 / 38.1 / 40.5, 192 rows 148 / 45.7 / 45.2;
+  // 64 dimensions, 64 rows 27.3 / 28.7 / 31.8, 128 rows 45.7 / 31.1 / 34.1.
+  auto wide_for = [&](int64_t rows) {
+    if (rows <= (a.head_dim == 64 ? 64 : 32)) return 0;
+    return rows > 128 && a.head_dim <= 128 ? 2 : 1;
+  };
+  // Chunk for `keys` keys of `blocks` row blocks: as many chunks as give each
+  // CU a 16-row workgroup (one workgroup's four waves keep 64 KB of a CU's
+  // loads out; more chunks only add joins: 1 x 30001 keys, 8 key heads of 128
+  // fp16 34 us with one workgroup a CU, 39 with two, 49 with four; 24 x 4111,
+  // 32 heads 158 / 158 / 173); for the wide kernel whole rounds over the CUs.
+  auto chunk_of = [&](int64_t keys, int64_t blocks, int wide) {
     const int64_t most = (keys + 127) / 128;
     int64_t parts = (num_cus + blocks - 1) / blocks;
+    if (wide) {
+      int64_t best = -1;
+      for (int64_t p = 1; p <= most && p <= 64; ++p) {
+        const int64_t chunk = ((keys + p - 1) / p + 127) / 128 * 128;
+        // a workgroup's fixed cost is about that of 256 keys
+        const int64_t cost = (blocks * p + num_cus - 1) / num_cus * (chunk + 256);
+        if (best < 0 || cost < best) {
+          best = cost;
+          parts = p;
+        }
+      }
+    }
     if (parts > most) parts = most;
     if (parts < 1) parts = 1;
     int64_t chunk = ((keys + parts - 1) / parts + 127) / 128 * 128;
     if (chunk > kAttnMaxChunk) chunk = kAttnMaxChunk;
     return (int)chunk;
   };
+  auto block_rows = [](int wide) { return wide ? 128 * wide : kRows; };
   a.group = a.n_q_heads / a.n_kv_heads;
   const int64_t prefix_rows = a.tokens * a.group, suffix_rows = a.max_q * a.group;
-  a.prefix_wide = a.suffix_wide = 0;
-  a.prefix_row_blocks = (int)((prefix_rows + kRows - 1) / kRows);
+  a.prefix_wide = wide_for(prefix_rows);
+  a.suffix_wide = wide_for(suffix_rows);
+  int64_t per = block_rows(a.prefix_wide);
+  a.prefix_row_blocks = (int)((prefix_rows + per - 1) / per);
   a.prefix_chunk = a.prefix_parts = 0;
   if (a.prefix_len > 0) {
-    a.prefix_chunk = chunk_of(a.prefix_len, (int64_t)a.prefix_row_blocks * a.n_kv_heads);
+    a.prefix_chunk = chunk_of(a.prefix_len, (int64_t)a.prefix_row_blocks * a.n_kv_heads, a.prefix_wide);
     a.prefix_parts = (int)((a.prefix_len + a.prefix_chunk - 1) / a.prefix_chunk);
   }
   a.prefix_items = (int64_t)a.prefix_row_blocks * a.n_kv_heads * a.prefix_parts;
-  a.suffix_row_blocks = (int)((suffix_rows + kRows - 1) / kRows);
-  a.suffix_chunk = chunk_of(max_suffix, a.batch * a.n_kv_heads * a.suffix_row_blocks);
+  per = block_rows(a.suffix_wide);
+  a.suffix_row_blocks = (int)((suffix_rows + per - 1) / per);
+  a.suffix_chunk = chunk_of(max_suffix, a.batch * a.n_kv_heads * a.suffix_row_blocks, a.suffix_wide);
   a.suffix_parts = (int)((max_suffix + a.suffix_chunk - 1) / a.suffix_chunk);
   a.suffix_items = a.batch * a.n_kv_heads * a.suffix_row_blocks * a.suffix_parts;
 }
