@@ -429,9 +429,8 @@ struct Wide {
   // a round is two tiles between barriers: K of it and of the tile after, V of
   // it, and the next round's two tiles of each on their way
   static constexpr int kStagesK = 5, kStagesV = 4;
-  // V's exponents and their inverse powers, of as many tiles as K
-  static constexpr int kScales = 2 * kKeys * 4;
-  static constexpr int kLds = (kStagesK + kStagesV) * kHalf + kStagesK * kScales;
+  static constexpr int kScales = kKeys * 4;         // V's scales beside its codes
+  static constexpr int kLds = (kStagesK + kStagesV) * kHalf + kStagesV * kScales;
 };
 
 // The rows of a wave again, if its mask's edge asks for it (whether it did). Item
@@ -507,16 +506,35 @@ __device__ __forceinline__ void wide_body(const AttnPrefixF8 &a, const Item &it,
   const int last_group = (it.c1 - 1) & ~7;
   typedef const __attribute__((address_space(4))) int32_t *constant_ptr;
   const constant_ptr pages = (constant_ptr)(uintptr_t)it.pages;
-  auto first_vector = [&](int j0, int i) {  // of the wave's group i of the tile at key j0
-    int j = j0 + 8 * (kGroups * wave + i);
-    j = j < last_group ? j : last_group;
-    const int32_t p = pages[j >> lg];
-    const int64_t page = (uint32_t)p < (uint32_t)a.num_pages ? p : 0;
-    return ((page * a.n_kv_heads + it.h) << lg) + (j & pmask);
+  // The page numbers of the wave's groups of a tile, one tile before they are
+  // needed; the groups' first vectors of the tile whose K goes out, and of the
+  // tile before, whose V goes out with it.
+  int32_t page_of[kGroups];
+  int64_t k_vec[kGroups], v_vec[kGroups];
+  auto key_of_group = [&](int tile, int i) {
+    const int j = it.c0 + tile * KT + 8 * (kGroups * wave + i);
+    return j < last_group ? j : last_group;
+  };
+  auto look_up = [&](int tile) {
+#pragma unroll
+    for (int i = 0; i < kGroups; ++i) page_of[i] = pages[key_of_group(tile, i) >> lg];
+  };
+  auto to_tile = [&](int tile) {
+#pragma unroll
+    for (int i = 0; i < kGroups; ++i) {
+      v_vec[i] = k_vec[i];
+      const int64_t page = (uint32_t)page_of[i] < (uint32_t)a.num_pages ? page_of[i] : 0;
+      k_vec[i] = ((page * a.n_kv_heads + it.h) << lg) + (key_of_group(tile, i) & pmask);
+    }
+    look_up(tile + 1);
   };
   struct Codes {  // of a tile, on their way
     u32x4 c[kLoads];
-    uint32_t s[kLoads], v;  // (K's scales, and V's beside them: logits take both)
+    uint32_t s[kLoads];
+  };
+  struct VCodes {
+    u32x4 c[kLoads];
+    u32x2 s[kLoads];  // fp16: the scales of the unit's eight keys; bf16: in [0], lane i's of key i
   };
   auto unit_of = [&](int i, int &group, int &u) {
     const int v = 64 * i + lane;
@@ -524,40 +542,37 @@ __device__ __forceinline__ void wide_body(const AttnPrefixF8 &a, const Item &it,
     u = kGroups > 1 ? v % (D / 2) : v;
     return kUnits % 64 == 0 || v < kUnits;
   };
-  auto load_k = [&](Codes &x, int j0) {
-    int64_t vec[kGroups];
-#pragma unroll
-    for (int g = 0; g < kGroups; ++g) vec[g] = first_vector(j0, g);
+  auto load_k = [&](Codes &x, int tile) {
+    to_tile(tile);
 #pragma unroll
     for (int i = 0; i < kLoads; ++i) {
       int g, u;
       if (!unit_of(i, g, u)) continue;
-      const int64_t at = kGroups > 1 && g ? vec[kGroups - 1] : vec[0];
+      const int64_t at = kGroups > 1 && g ? k_vec[kGroups - 1] : k_vec[0];
       x.c[i] = *reinterpret_cast<const u32x4 *>(kc + at * D + 16 * u);
       x.s[i] = a.k_scales[at + u / (D / 16)];
     }
-    // V's scales: lane i of the wave has that of key i of its groups
-    const int64_t at = kGroups > 1 && (lane & 8) ? vec[kGroups - 1] : vec[0];
-    x.v = a.v_scales[at + (lane & 7)];
   };
-  auto load_v = [&](Codes &x, int j0) {
-    int64_t vec[kGroups];
-#pragma unroll
-    for (int g = 0; g < kGroups; ++g) vec[g] = first_vector(j0, g);
+  constexpr bool kScaled = __is_same(T, TypeF16);  // V's scales are in its LDS tiles
+  auto load_v = [&](VCodes &x) {  // of the tile before load_k's
 #pragma unroll
     for (int i = 0; i < kLoads; ++i) {
       int g, u;
       if (!unit_of(i, g, u)) continue;
-      const int64_t at = kGroups > 1 && g ? vec[kGroups - 1] : vec[0];
+      const int64_t at = kGroups > 1 && g ? v_vec[kGroups - 1] : v_vec[0];
       x.c[i] = *reinterpret_cast<const u32x4 *>(vc + at * D + 16 * u);
+      if constexpr (kScaled) x.s[i] = *reinterpret_cast<const u32x2 *>(a.v_scales + at);
+    }
+    if constexpr (!kScaled) {
+      const int64_t at = kGroups > 1 && (lane & 8) ? v_vec[kGroups - 1] : v_vec[0];
+      x.s[0][0] = a.v_scales[at + (lane & 7)];
     }
   };
   uint8_t *const vsmem = smem + C::kStagesK * C::kHalf;
   uint8_t *const ssmem = vsmem + C::kStagesV * C::kHalf;
   auto k_stage = [&](int tile) { return smem + tile % C::kStagesK * C::kHalf; };
   auto v_stage = [&](int tile) { return vsmem + tile % C::kStagesV * C::kHalf; };
-  // exponents [KT], and inverse powers [KT]
-  auto s_stage = [&](int tile) { return reinterpret_cast<float *>(ssmem + tile % C::kStagesK * C::kScales); };
+  auto s_stage = [&](int tile) { return reinterpret_cast<float *>(ssmem + tile % C::kStagesV * C::kScales); };
   auto store_k = [&](const Codes &x, int tile) {
     uint8_t *st = k_stage(tile);
 #pragma unroll
@@ -570,15 +585,12 @@ __device__ __forceinline__ void wide_body(const AttnPrefixF8 &a, const Item &it,
       *reinterpret_cast<vec8 *>(to + 16 * (chunk ^ swz(key))) = values8<T>(u32x2{x.c[i][0], x.c[i][1]}, f);
       *reinterpret_cast<vec8 *>(to + 16 * ((chunk + 1) ^ swz(key))) = values8<T>(u32x2{x.c[i][2], x.c[i][3]}, f);
     }
-    if (lane < 8 * kGroups) {
-      float *sc = s_stage(tile) + 8 * kGroups * wave + lane;
-      const uint32_t b = x.v < 253u ? x.v : 253u;  // (of a key that is not seen anything)
-      sc[0] = (float)((int)b - 127);
-      sc[KT] = scale_inverse(b);
-    }
   };
-  auto store_v = [&](const Codes &x, int tile, int j0) {
+  // A scale as it counts: a key that is not seen may have any byte beside its codes.
+  auto v_scale = [](uint32_t b) { return scale_of(b < 253u ? b : 253u); };
+  auto store_v = [&](const VCodes &x, int tile) {
     uint8_t *st = v_stage(tile);
+    const int j0 = it.c0 + tile * KT;
 #pragma unroll
     for (int i = 0; i < kLoads; ++i) {
       int g, u;
@@ -587,10 +599,21 @@ __device__ __forceinline__ void wide_body(const AttnPrefixF8 &a, const Item &it,
       const int group = kGroups * wave + g, valid = it.c1 - (j0 + 8 * group);
       const uint32_t lo = valid >= 4 ? ~0u : valid <= 0 ? 0u : ~0u >> (32 - 8 * valid);
       const uint32_t hi = valid >= 8 ? ~0u : valid <= 4 ? 0u : ~0u >> (64 - 8 * valid);
+      const u32x2 c0 = {x.c[i][0] & lo, x.c[i][1] & hi}, c1 = {x.c[i][2] & lo, x.c[i][3] & hi};
       vec8 *to = reinterpret_cast<vec8 *>(st + (group * D + 2 * u) * 16);
-      to[0] = values8<T>(u32x2{x.c[i][0] & lo, x.c[i][1] & hi}, 1.0f);
-      to[1] = values8<T>(u32x2{x.c[i][2] & lo, x.c[i][3] & hi}, 1.0f);
+      if constexpr (kScaled) {
+        float f[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) f[e] = v_scale(x.s[i][e >> 2] >> 8 * (e & 3) & 255u);
+        to[0] = values8_each(c0, f);
+        to[1] = values8_each(c1, f);
+      } else {
+        to[0] = values8<T>(c0, 1.0f);
+        to[1] = values8<T>(c1, 1.0f);
+      }
     }
+    if constexpr (!kScaled)
+      if (lane < 8 * kGroups) s_stage(tile)[8 * kGroups * wave + lane] = v_scale(x.s[0][0]);
   };
 
   float16_t o[R][kDT];
@@ -631,24 +654,18 @@ __device__ __forceinline__ void wide_body(const AttnPrefixF8 &a, const Item &it,
     }
   };
   const int plain_end = it.c1 < all_see ? it.c1 : all_see;  // steps up to here need no mask
-  // Half c of a step's keys: this lane's eight (exponents, or inverse powers at + KT).
-  auto eight = [&](const float *sc, int sub, int c, float (&x)[8]) {
-    const float4_t *p = reinterpret_cast<const float4_t *>(sc + 32 * sub + 16 * c + 8 * h);
-    const float4_t lo = p[0], hi = p[1];
-#pragma unroll
-    for (int e = 0; e < 4; ++e) x[e] = lo[e], x[4 + e] = hi[e];
-  };
-
-  // One step: the weights of s (32 keys, V at vs + `sub`, scales sv) on the vector
-  // ALU beside the logits of the next 32 keys (from jn, K at kn + `nsub`; past the
-  // last key: of what is there, masked) on the matrix cores, then the products
-  // with V beside the next logits' scales (sn) and maximum. Each half reads the
-  // next one's operands from LDS, the last one those of K for the step after (K at
-  // ka + `asub`; one-step tiles read them at the step's start, behind the barrier).
+  // One step: the weights of s (32 keys, V at vs + `sub`, its scales sv) on the
+  // vector ALU beside the logits of the next 32 keys (from jn, K at kn + `nsub`; past
+  // the last key: of what is there, masked) on the matrix cores, then the products
+  // with V beside the next maximum. Each half reads the next one's operands from
+  // LDS, the last one those of K for the step after (K at ka + `asub`; one-step tiles
+  // read them at the step's start, behind the barrier).
+  // `first` and `second`, work on the tiles to come, go beside the products with V.
   constexpr bool kCarry = KT == 64;
   vec8 k0[kM];
   auto step = [&](const uint8_t *vs, const float *sv, int sub, const Logits &s, const uint8_t *kn,
-                  const float *sn, int nsub, int jn, Logits &next, const uint8_t *ka, int asub) {
+                  int nsub, int jn, Logits &next, const uint8_t *ka, int asub, auto first,
+                  auto second) {
     bool grown = false;
 #pragma unroll
     for (int w = 0; w < R; ++w) grown = grown || top[w] > m[w] + kSlack;
@@ -675,8 +692,11 @@ __device__ __forceinline__ void wide_body(const AttnPrefixF8 &a, const Item &it,
     __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
     for (int c = 0; c < 2; ++c) {
-      float back[8];
-      eight(sv + KT, sub, c, back);
+      float4_t vs_lo, vs_hi;  // this lane's eight keys' scales
+      if constexpr (!kScaled) {
+        const float4_t *f = reinterpret_cast<const float4_t *>(sv + 32 * sub + 16 * c + 8 * h);
+        vs_lo = f[0], vs_hi = f[1];
+      }
       if (c == 0) {
 #pragma unroll
         for (int i = 0; i < kM; ++i) k1[i] = k_operand(kn, nsub, kM + i);
@@ -691,16 +711,18 @@ __device__ __forceinline__ void wide_body(const AttnPrefixF8 &a, const Item &it,
           next[w] = T::mfma32(c == 0 ? k0[i] : k1[i], q[w][c * kM + i], c + i == 0 ? float16_t{} : next[w]);
 #pragma unroll
       for (int w = 0; w < R; ++w) {
+        float sum = 0.f;
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
-          const float x = __builtin_amdgcn_exp2f(s[w][8 * c + e] - ref[w]);
-          l[w] = fmaf(x, back[e], l[w]);
-          p[w][c][e] = (elem)x;
+          const float x = __builtin_amdgcn_exp2f(fmaf(s[w][8 * c + e], a.scale_log2, -ref[w]));
+          sum += x;
+          p[w][c][e] = (elem)(kScaled ? x : x * (e < 4 ? vs_lo[e & 3] : vs_hi[e & 3]));
         }
+        l[w] += sum;
         asm volatile("" : "+v"(p[w][c]));  // computed here, not after the mask's branch
       }
       // matrix and vector instructions in turn
-      __builtin_amdgcn_sched_group_barrier(0x100, kM + 2, 0);
+      __builtin_amdgcn_sched_group_barrier(0x100, kM + (kScaled ? 0 : 2), 0);
 #pragma unroll
       for (int i = 0; i < R * kM; ++i) {
         __builtin_amdgcn_sched_group_barrier(0x8, 1, 0);
@@ -714,8 +736,6 @@ __device__ __forceinline__ void wide_body(const AttnPrefixF8 &a, const Item &it,
     for (int w = 0; w < R; ++w) x[w] = -INFINITY;
 #pragma unroll
     for (int c = 0; c < 2; ++c) {
-      float ex[8];
-      eight(sn, nsub, c, ex);
       if (c == 0) {
 #pragma unroll
         for (int i = 0; i < kDT; ++i) vf[1][i] = v_operand(vs, 2 * sub + 1, i);
@@ -730,45 +750,41 @@ __device__ __forceinline__ void wide_body(const AttnPrefixF8 &a, const Item &it,
 #pragma unroll
       for (int w = 0; w < R; ++w)
 #pragma unroll
-        for (int e = 0; e < 8; e += 2) {
-          const float y0 = fmaf(next[w][8 * c + e], a.scale_log2, ex[e]);
-          const float y1 = fmaf(next[w][8 * c + e + 1], a.scale_log2, ex[e + 1]);
-          next[w][8 * c + e] = y0, next[w][8 * c + e + 1] = y1;
-          x[w] = fmaxf(fmaxf(y0, y1), x[w]);
-        }
-      __builtin_amdgcn_sched_group_barrier(0x100, kDT + 2, 0);
+        for (int e = 0; e < 8; e += 2)
+          x[w] = fmaxf(fmaxf(next[w][8 * c + e], next[w][8 * c + e + 1]), x[w]);
+      if (c == 0) first();
+      else second();
+      __builtin_amdgcn_sched_group_barrier(0x100, kDT, 0);
 #pragma unroll
       for (int i = 0; i < R * kDT; ++i) {
         __builtin_amdgcn_sched_group_barrier(0x8, 1, 0);
-        __builtin_amdgcn_sched_group_barrier(0x2, 4, 0);
+        __builtin_amdgcn_sched_group_barrier(0x2, 32 / (R * kDT), 0);
       }
       __builtin_amdgcn_sched_barrier(0);
     }
 #pragma unroll
-    for (int w = 0; w < R; ++w) top[w] = max_over_halves(x[w]);
+    for (int w = 0; w < R; ++w) top[w] = max_over_halves(x[w]) * a.scale_log2;
   };
 
-  // K is used up to one tile before V: what goes out together is K of tile p + 1
-  // and V of tile p.
+  // K is used up to one tile before V.
   const int tiles = (it.c1 - it.c0 + KT - 1) / KT;
   Logits s, s2;
-  Codes xk, xv;
-  auto load_pair = [&](int p) {
-    load_k(xk, it.c0 + (p + 1) * KT);
-    load_v(xv, it.c0 + p * KT);
-  };
-  auto store_pair = [&](int p) {
-    store_k(xk, p + 1);
-    store_v(xv, p, it.c0 + p * KT);
-  };
+  Codes xk;
+  VCodes xv;
   if (tiles > 0) {
-    load_k(xk, it.c0);
+    look_up(0);
+    load_k(xk, 0);
     store_k(xk, 0);
-    load_pair(0);
-    store_pair(0);
-    load_pair(1);
-    if (tiles > 1) store_pair(1);
-    load_pair(2);
+    load_k(xk, 1);
+    load_v(xv);
+    store_k(xk, 1);
+    store_v(xv, 0);
+    load_k(xk, 2);
+    load_v(xv);
+    store_k(xk, 2);
+    store_v(xv, 1);
+    load_k(xk, 3);
+    load_v(xv);
     __syncthreads();
 #pragma unroll
     for (int i = 0; i < kQ; ++i) {
@@ -779,45 +795,41 @@ __device__ __forceinline__ void wide_body(const AttnPrefixF8 &a, const Item &it,
     if (it.c0 + 32 > plain_end) mask(it.c0, s);
 #pragma unroll
     for (int w = 0; w < R; ++w) {
-      float x = -INFINITY;
+      float x = s[w][0];
 #pragma unroll
-      for (int c = 0; c < 2; ++c) {
-        float ex[8];
-        eight(s_stage(0), 0, c, ex);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          s[w][8 * c + e] = fmaf(s[w][8 * c + e], a.scale_log2, ex[e]);
-          x = fmaxf(x, s[w][8 * c + e]);
-        }
-      }
-      top[w] = max_over_halves(x);
+      for (int r = 1; r < 16; ++r) x = fmaxf(x, s[w][r]);
+      top[w] = max_over_halves(x) * a.scale_log2;
     }
     if constexpr (kCarry) {
 #pragma unroll
       for (int i = 0; i < kM; ++i) k0[i] = k_operand(smem, 1, i);
     }
   }
-  for (int round = 0; round < tiles; round += 2) {
-    if (round) __syncthreads();
+#pragma unroll 1
+  for (int kt = 0; kt < tiles; ++kt) {  // (two tiles between barriers)
+    if (kt && (kt & 1) == 0) __syncthreads();
+    const int j0 = it.c0 + kt * KT;
+    const uint8_t *vs = v_stage(kt), *kn = k_stage(kt + 1);
+    const float *sv = s_stage(kt);
+    // K of the tile three ahead and V of the one two ahead have come: they go to
+    // LDS, and the next ones out. (Past the last tile too: what is written there is
+    // not read, and what is loaded is the last group again.)
+    auto k_on = [&]() {
+      store_k(xk, kt + 3);
+      load_k(xk, kt + 4);
+    };
+    auto v_on = [&]() {
+      store_v(xv, kt + 2);
+      load_v(xv);
+    };
+    auto nothing = []() {};
+    if constexpr (KT == 64) {
+      step(vs, sv, 0, s, k_stage(kt), 1, j0 + 32, s2, kn, 0, nothing, k_on);
+      step(vs, sv, 1, s2, kn, 0, j0 + 64, s, kn, 1, v_on, nothing);
+    } else {
+      step(vs, sv, 0, s, kn, 0, j0 + 32, s2, nullptr, 0, k_on, v_on);
 #pragma unroll
-    for (int b = 0; b < 2; ++b) {
-      const int kt = round + b, j0 = it.c0 + kt * KT;
-      if (kt >= tiles) break;
-      const uint8_t *vs = v_stage(kt), *kn = k_stage(kt + 1);
-      const float *sv = s_stage(kt), *sn = s_stage(kt + 1);
-      if constexpr (KT == 64) {
-        step(vs, sv, 0, s, k_stage(kt), sv, 1, j0 + 32, s2, kn, 0);
-        step(vs, sv, 1, s2, kn, sn, 0, j0 + 64, s, kn, 1);
-      } else {
-        step(vs, sv, 0, s, kn, sn, 0, j0 + 32, s2, nullptr, 0);
-#pragma unroll
-        for (int w = 0; w < R; ++w) s[w] = s2[w];
-      }
-      // the pair of the tile two ahead, whose codes have come; the next one goes out
-      if (kt + 2 < tiles) {
-        store_pair(kt + 2);
-        load_pair(kt + 3);
-      }
+      for (int w = 0; w < R; ++w) s[w] = s2[w];
     }
   }
 

@@ -65,6 +65,20 @@ __device__ __forceinline__ typename T::vec8 values8(u32x2 c, float scale) {
   }
   return v;
 }
+// Eight codes as fp16 values, each times a power of two of its own.
+__device__ __forceinline__ half8_t values8_each(u32x2 c, const float (&scale)[8]) {
+  half8_t v;
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    half2_t a = {0, 0}, b = {0, 0};
+    a = __builtin_amdgcn_cvt_scalef32_f16_fp8(a, (int)c[i], scale[4 * i], 0, false);
+    a = __builtin_amdgcn_cvt_scalef32_f16_fp8(a, (int)c[i], scale[4 * i + 1], 1, true);
+    b = __builtin_amdgcn_cvt_scalef32_f16_fp8(b, (int)c[i], scale[4 * i + 2], 2, false);
+    b = __builtin_amdgcn_cvt_scalef32_f16_fp8(b, (int)c[i], scale[4 * i + 3], 3, true);
+    v[4 * i] = a[0], v[4 * i + 1] = a[1], v[4 * i + 2] = b[0], v[4 * i + 3] = b[1];
+  }
+  return v;
+}
 // Eight codes as fp32 values.
 __device__ __forceinline__ void values8(u32x2 c, float scale, float (&x)[8]) {
 #pragma unroll

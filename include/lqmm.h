@@ -421,10 +421,9 @@ lqmm_status lqmm_kv_read_f8(const uint8_t *k_cache, const uint8_t *v_cache, cons
 
 /*
  * lqmm_attn_prefix over the 8-bit cache; `type` (fp16 or bf16) is that of q and
- * out. A key enters the products as its value rounded to `type` (exact but for
- * fp16 values below 2^-14, in steps of 2^-24); V's codes enter as they are, and
- * their scales count in the softmax's weights before these are rounded to
- * `type`. The rest is as for lqmm_attn_prefix, a NaN code being a NaN value.
+ * out. Keys and values enter the products exactly, but for fp16 values below
+ * 2^-14, which may enter in steps of 2^-24. The rest is as for lqmm_attn_prefix, a
+ * NaN code being a NaN value.
  */
 lqmm_status lqmm_attn_prefix_f8(const void *q, int64_t ldq, const uint8_t *k_cache,
                                 const uint8_t *v_cache, const uint8_t *k_scales,

@@ -118,7 +118,9 @@ def attention(q, cache, pages, lens, prefix_pages, prefix_len, q_start, scale, t
     most 448: the largest is held at 2^6 or more in fp16 (2^14, and a reference up
     to 2^8 above it), whose steps end at 2^-24, so that a weight is off by 2^-25 /
     2^6 = 2^-31 of the largest; at 2^-8 or more in bf16, where exp2 ends at the
-    least normal number, 2^-126, so that 2^-118 of the largest vanishes."""
+    least normal number, 2^-126, so that 2^-118 of the largest vanishes. In fp16 a
+    value of V below 2^-14 may enter in steps of 2^-24, off by 2^-25, and so their
+    mean."""
     T, Hq, D = q.shape
     Hkv = cache[0].shape[1]
     G = Hq // Hkv
@@ -152,6 +154,8 @@ def attention(q, cache, pages, lens, prefix_pages, prefix_len, q_start, scale, t
                 bo[r, h] += (2 * S + 2 * E + 2.0 ** -21 + U[t]) * a + U[t] * np.abs(out[r, h])
                 w = np.exp2(y - y.max())
                 lost = 2.0 ** -31 if t == "f16" else 2.0 ** -118
+                if t == "f16":
+                    bo[r, h] += 2.0 ** -25
                 bo[r, h] += len(z) * lost * 448 * np.exp2(y.max() - m / np.log(2)) / total
                 S = S + E
                 bl[r, h] = S + 2.0 ** -20 + 2.0 ** -22 * abs(lse[r, h]) + len(z) * 2.0 ** -118 / w.sum()
