@@ -394,7 +394,7 @@ __device__ __forceinline__ void rows16_body(const AttnPrefixF8 &a, const Item &i
 }
 
 template <class T, int D>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kThreads, D <= 128 ? 2 : 1)
 attn_f8_rows16_kernel(AttnPrefixF8 a, uint32_t item0) {
   __shared__ Rows16<D, kThreads / 64> sm;
   Item it;
@@ -897,6 +897,70 @@ attn_f8_wide_kernel(AttnPrefixF8 a, uint32_t item0) {
     wide_body<T, D, NW, R>(a, it, item0, smem);
 }
 
+// Joins the partial results of each row. D / 4 threads take a part, four
+// dimensions each, and `slots` such groups share a row's parts, so that a row of
+// many parts is a few round trips to memory (one conversation of 30001 keys, 32
+// parts of 32 rows: with one group a row the join is half of the call). Groups'
+// sums are added in LDS in a fixed order. Weights as in attn_join_kernel.
+template <int D>
+constexpr int kJoinGroups = D == 64 ? 16 : D <= 128 ? 8 : 4;
+
+template <class T, int D>
+__global__ void __launch_bounds__(kThreads)
+attn_f8_join_kernel(AttnPrefix a, uint32_t first, int slots) {
+  typedef typename T::elem elem;
+  constexpr int kPer = D / 4, kGroups = kJoinGroups<D>;
+  __shared__ float top[kGroups], sum[kGroups];
+  __shared__ __attribute__((aligned(16))) float part[kGroups][D];
+  const int group = threadIdx.x / kPer, slot = group % slots;
+  const int64_t nrows = a.tokens * a.n_q_heads;
+  const int64_t row = (int64_t)(first + blockIdx.x) * (kGroups / slots) + group / slots;
+  const int d = 4 * (threadIdx.x % kPer);
+  const bool live = group < kGroups && row < nrows;
+  const int parts = a.prefix_parts + a.suffix_parts;
+  float m = -INFINITY;
+  if (live) {
+#pragma unroll 4
+    for (int p = slot; p < parts; p += slots) m = fmaxf(m, a.part_ml[p * nrows + row].x);
+    if (d == 0) top[group] = m;
+  }
+  __syncthreads();
+  float l = 0.f;
+  float4_t o = {0.f, 0.f, 0.f, 0.f};
+  if (live) {
+    for (int i = group - slot; i < group - slot + slots; ++i) m = fmaxf(m, top[i]);
+#pragma unroll 4
+    for (int p = slot; p < parts; p += slots) {
+      // of a part that sees no key nothing counts
+      const float2 ml = a.part_ml[p * nrows + row];
+      const float4_t x = *reinterpret_cast<const float4_t *>(a.part_o + (p * nrows + row) * D + d);
+      const bool seen = ml.y != 0.f;
+      const float w = seen ? __builtin_amdgcn_exp2f(ml.x - m) * kJoinWeight : 0.f;
+      l += w * (seen ? ml.y : 0.f);
+#pragma unroll
+      for (int r = 0; r < 4; ++r) o[r] += w * (seen ? x[r] : 0.f);
+    }
+    *reinterpret_cast<float4_t *>(&part[group][d]) = o;
+    if (d == 0) sum[group] = l;
+  }
+  __syncthreads();
+  if (!live || slot) return;
+  for (int i = 1; i < slots; ++i) {
+    l += sum[group + i];
+    o += *reinterpret_cast<const float4_t *>(&part[group + i][d]);
+  }
+  // of a row of no sequence nothing read above counts
+  if (a.q_start && a.part_ml[a.prefix_parts * nrows + row].y == kNoSequence) {
+    l = 0.f;
+    o = float4_t{0.f, 0.f, 0.f, 0.f};
+  }
+  const float inv = l == 0.f ? 0.f : 1.0f / l;
+  typedef elem vec4 __attribute__((ext_vector_type(4)));
+  *reinterpret_cast<vec4 *>(static_cast<elem *>(a.out) + row * D + d) =
+      vec4{(elem)(o[0] * inv), (elem)(o[1] * inv), (elem)(o[2] * inv), (elem)(o[3] * inv)};
+  if (a.lse && d == 0) a.lse[row] = lse_of(m, l * (1 << kJoinShift));
+}
+
 template <class T, int D, int NW, int R>
 hipError_t launch_wide(const AttnPrefixF8 &a, int64_t item0, int64_t items, hipStream_t stream) {
   constexpr auto kern = attn_f8_wide_kernel<T, D, NW, R>;
@@ -938,11 +1002,11 @@ hipError_t launch(const AttnPrefixF8 &a, hipStream_t stream) {
     e = launch_items<T, D>(a, a.suffix_wide, a.prefix_items, a.suffix_items, stream);
   }
   if (e != hipSuccess || a.prefix_parts + a.suffix_parts == 1) return e;
-  constexpr int kRowsPerBlock = kThreads / (D / 4);
-  const int64_t nrows = a.tokens * a.n_q_heads;
-  return launch_in_pieces((nrows + kRowsPerBlock - 1) / kRowsPerBlock, kThreads,
-                          [&](uint32_t first, unsigned n) {
-    hipLaunchKernelGGL((attn_join_kernel<T, D>), dim3(n), dim3(kThreads), 0, stream, a, first);
+  int slots = 1;
+  while (slots < kJoinGroups<D> && 2 * slots <= a.prefix_parts + a.suffix_parts) slots *= 2;
+  const int64_t rows = a.tokens * a.n_q_heads, per = kJoinGroups<D> / slots;
+  return launch_in_pieces((rows + per - 1) / per, kThreads, [&](uint32_t first, unsigned n) {
+    hipLaunchKernelGGL((attn_f8_join_kernel<T, D>), dim3(n), dim3(kThreads), 0, stream, a, first, slots);
   });
 }
 
@@ -971,11 +1035,15 @@ void attn_f8_plan(AttnPrefixF8 &a, int64_t max_suffix, int num_cus) {
     if (rows <= (a.head_dim == 64 ? 64 : 32)) return 0;
     return rows > 128 && a.head_dim <= 128 ? 2 : 1;
   };
-  // Chunk for `keys` keys of `blocks` row blocks: as many chunks as give each
-  // CU a 16-row workgroup (one workgroup's four waves keep 64 KB of a CU's
-  // loads out; more chunks only add joins: 1 x 30001 keys, 8 key heads of 128
-  // fp16 34 us with one workgroup a CU, 39 with two, 49 with four; 24 x 4111,
-  // 32 heads 158 / 158 / 173); for the wide kernel whole rounds over the CUs.
+  // Chunk for `keys` keys of `blocks` row blocks. 16-row kernel: as many chunks as
+  // give each CU a workgroup. With few blocks more chunks cost more at the join
+  // than they gain (1 x 30001 keys, 8 key heads of 128 fp16: 18.6 us with one
+  // workgroup a CU, 22 with two, 26 with four), with many one chunk a sequence is
+  // near the cache's read (64 x 8001 ragged: 108 us, 126 with two to four). Once
+  // a sequence is cut, it is into chunks of at most 2048 keys: lengths differ, and
+  // the call ends with the longest chunks (24 x 8209 ragged, 8 key heads: 52.8 us,
+  // 59.5 with two chunks; 32 key heads 168, 230 with two; 64 x 12001, 8 key heads
+  // 170, 214 with two). Wide kernel: whole rounds over the CUs.
   auto chunk_of = [&](int64_t keys, int64_t blocks, int wide) {
     const int64_t most = (keys + 127) / 128;
     int64_t parts = (num_cus + blocks - 1) / blocks;
@@ -990,6 +1058,10 @@ void attn_f8_plan(AttnPrefixF8 &a, int64_t max_suffix, int num_cus) {
           parts = p;
         }
       }
+    }
+    if (!wide && (parts > 1 || keys > kAttnMaxChunk)) {
+      const int64_t cut = (keys + 2047) / 2048;
+      if (parts < cut) parts = cut;
     }
     if (parts > most) parts = most;
     if (parts < 1) parts = 1;
