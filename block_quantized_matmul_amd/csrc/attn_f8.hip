@@ -1026,14 +1026,32 @@ hipError_t launch_dim(const AttnPrefixF8 &a, hipStream_t stream) {
 // Splits the keys so that the launch fills the chip. A chunk is a multiple of
 // 128 keys and at most kAttnMaxChunk.
 void attn_f8_plan(AttnPrefixF8 &a, int64_t max_suffix, int num_cus) {
-  // Rows of a work item: 16 while reading the cache is the cost, else 128 or
-  // 256 (wide 1, 2). Measured, a prefix of 16001 keys, 8 key heads, fp16 (us;
-  // 16-row / 128 / 256): 128 dimensions, 32 rows 29.5 / 33.6 / 35.3, 48 rows
-  // 37.3 / 34.5 / 36.2, 128 rows 81 / 38.1 / 40.5, 192 rows 148 / 45.7 / 45.2;
-  // 64 dimensions, 64 rows 27.3 / 28.7 / 31.8, 128 rows 45.7 / 31.1 / 34.1.
-  auto wide_for = [&](int64_t rows) {
-    if (rows <= (a.head_dim == 64 ? 64 : 32)) return 0;
-    return rows > 128 && a.head_dim <= 128 ? 2 : 1;
+  // Rows of a work item: 16, 128 or 256 (wide 0, 1, 2), the least of an estimate
+  // fitted to measured calls: a fixed time and one for each row block, key and
+  // head (ps), to which an item's start counts as some 250 keys. 16 rows read the
+  // cache again for every 16; the others wait longer for their tiles, of which a
+  // work item has eight or more if there are keys. Measured, 8 key heads, fp16
+  // (us; 16 / 128 / 256):
+  // 128 dimensions, 60001 keys, 64 rows 59 / 80 / 79, 128 rows 99 / 83 / 85,
+  // 256 rows 174 / 142 / 94; 16001 keys, 128 rows 30 / 35 / 34, 256 rows
+  // 52 / 50 / 41; 4001 keys, 384 rows 29 / 38 / 36; 64 dimensions, 60001 keys,
+  // 64 rows 35 / 51 / 59, 128 rows 59 / 53 / 61, 256 rows 102 / 91 / 65; 32 x 64
+  // keys, 128 rows each 18 / 14, 256 rows 30 / - / 17.
+  auto wide_for = [&](int64_t rows, int64_t sequences, int64_t keys) {
+    struct Cost {
+      int rows16, rows128, rows256;
+    };
+    const Cost c = a.head_dim == 64   ? Cost{12, 83, 100}
+                   : a.head_dim == 96 ? Cost{15, 120, 158}
+                   : a.head_dim == 128 ? Cost{20, 130, 130}
+                                       : Cost{47, 242, 0};
+    const double all = (double)sequences * a.n_kv_heads * (keys + 250);
+    const double tiles = 27e3 * (keys < 512 ? keys : 512);
+    const double few = 12e6 + c.rows16 * all * ((rows + 15) / 16);
+    const double mid = 6e6 + tiles + c.rows128 * all * ((rows + 127) / 128);
+    const double many = 16e6 + tiles + c.rows256 * all * ((rows + 255) / 256);
+    if (c.rows256 && many < mid && many < few) return 2;
+    return mid < few ? 1 : 0;
   };
   // Chunk for `keys` keys of `blocks` row blocks. 16-row kernel: as many chunks as
   // give each CU a workgroup. With few blocks more chunks cost more at the join
@@ -1072,8 +1090,8 @@ void attn_f8_plan(AttnPrefixF8 &a, int64_t max_suffix, int num_cus) {
   auto block_rows = [](int wide) { return wide ? 128 * wide : kRows; };
   a.group = a.n_q_heads / a.n_kv_heads;
   const int64_t prefix_rows = a.tokens * a.group, suffix_rows = a.max_q * a.group;
-  a.prefix_wide = wide_for(prefix_rows);
-  a.suffix_wide = wide_for(suffix_rows);
+  a.prefix_wide = wide_for(prefix_rows, 1, a.prefix_len);
+  a.suffix_wide = wide_for(suffix_rows, a.batch, max_suffix);
   int64_t per = block_rows(a.prefix_wide);
   a.prefix_row_blocks = (int)((prefix_rows + per - 1) / per);
   a.prefix_chunk = a.prefix_parts = 0;
