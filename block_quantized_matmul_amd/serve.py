@@ -6,6 +6,12 @@ behind one shared prompt, from the library's serving operators:
   (lqmm_kv_append) -> attention, the shared prompt's keys read once for the
   whole batch (lqmm_attn_prefix) -> e4m3 -> output product.
 
+Each half has a form in fewer bits: weight_bits=4 takes the products from
+microscaled 4-bit floats (lqmm_quant_mxfp4, lqmm_gemm_mxfp4), kv_bits=8 keeps
+the cache as e4m3 codes (lqmm_kv_append_norm, lqmm_attn_prefix_f8, and
+lqmm_kv_read_f8 for what it holds); q_norm and k_norm normalize the heads of q
+and k before the rotation (lqmm_kv_append_norm).
+
 The caches, tables and lengths are device tensors made when the block is built,
 and a step reads its lengths and pages from them, so that one captured HIP graph
 serves every later step behind a prompt of the same length. What a step computes
@@ -37,20 +43,37 @@ def quantize_weight_f8b128(w):
 class SharedPromptAttention:
     """wqkv: ((n_q_heads + 2 n_kv_heads) * head_dim, hidden) and wo: (hidden,
     n_q_heads * head_dim) float weights; `batch` conversations of at most
-    `max_pages` pages each behind one prompt; fp16 activations."""
+    `max_pages` pages each behind one prompt; fp16 activations. weight_bits: 8
+    (e4m3, blocks of 128) or 4 (microscaled floats; hidden % 32 == 0); kv_bits:
+    16 or 8; q_norm, k_norm: weights (head_dim,) of the norms of q's and k's
+    heads with `eps`, None: no norm."""
 
     def __init__(self, wqkv, wo, n_q_heads, n_kv_heads, head_dim, batch, prompt_pages, max_pages,
-                 page_size=16, rope_base=10000.0):
+                 page_size=16, rope_base=10000.0, weight_bits=8, kv_bits=16, q_norm=None, k_norm=None,
+                 eps=1e-6):
         import torch
 
         import block_quantized_matmul_amd as bq
+        if weight_bits not in (4, 8) or kv_bits not in (8, 16):
+            raise ValueError("weight_bits is 4 or 8, kv_bits 8 or 16")
         self.torch, self.bq = torch, bq
+        self.weight_bits, self.kv_bits, self.eps = weight_bits, kv_bits, eps
         self.hq, self.hkv, self.d, self.ps = n_q_heads, n_kv_heads, head_dim, page_size
         self.dev = wqkv.device
-        self.wqkv, self.wqkv_scale = quantize_weight_f8b128(wqkv)
-        self.wo, self.wo_scale = quantize_weight_f8b128(wo)
-        self.k_cache, self.v_cache = bq.kv_cache_empty(prompt_pages + batch * max_pages, n_kv_heads,
-                                                       page_size, head_dim, device=self.dev)
+        self.q_norm, self.k_norm = (
+            None if w is None else w.to(device=self.dev, dtype=torch.float32).contiguous()
+            for w in (q_norm, k_norm))
+        quantize = quantize_weight_f8b128 if weight_bits == 8 else bq.lqmm_quant_mxfp4
+        self.wqkv, self.wqkv_scale = quantize(wqkv)
+        self.wo, self.wo_scale = quantize(wo)
+        # the cache: (k, v), in 8 bits (k, v, k_scales, v_scales)
+        of, num_pages = dict(device=self.dev), prompt_pages + batch * max_pages
+        if kv_bits == 8:
+            of["dtype"] = torch.float8_e4m3fn
+        self.cache = bq.kv_cache_empty(num_pages, n_kv_heads, page_size, head_dim, **of)
+        self.k_cache, self.v_cache = self.cache
+        if kv_bits == 8:
+            self.cache += bq.kv_scales_empty(num_pages, n_kv_heads, page_size, device=self.dev)
         inv_freq = rope_base ** (-np.arange(0, head_dim, 2) / head_dim)
         self.turns = bq.lqmm_rope_turns(inv_freq, device=self.dev)
         i32 = dict(dtype=torch.int32, device=self.dev)
@@ -65,16 +88,29 @@ class SharedPromptAttention:
         self.prompt_len = 0
         self.rows = torch.arange(batch, device=self.dev)
 
+    def _product(self, w, scale, x):
+        if self.weight_bits == 4:
+            return self.bq.lqmm_gemm_mxfp4(w, scale, *self.bq.lqmm_quant_mxfp4(x))
+        return self.bq.lqmm_gemm_f8b128(w, scale, *self.bq.lqmm_quant_f8b128(x))
+
     def _project(self, x):
         """x (T, hidden) -> views q, k, v of the product's rows."""
-        codes, scales = self.bq.lqmm_quant_f8b128(x)
-        y = self.bq.lqmm_gemm_f8b128(self.wqkv, self.wqkv_scale, codes, scales)
-        y = y.view(x.shape[0], self.hq + 2 * self.hkv, self.d)
+        y = self._product(self.wqkv, self.wqkv_scale, x).view(x.shape[0], self.hq + 2 * self.hkv, self.d)
         return y[:, :self.hq], y[:, self.hq:self.hq + self.hkv], y[:, self.hq + self.hkv:]
 
+    def _append(self, q, k, v, positions, slots):
+        """Norms, rotation and append; returns q as the attention reads it."""
+        if self.kv_bits == 16 and self.q_norm is None and self.k_norm is None:
+            return self.bq.lqmm_kv_append(q, k, v, positions, slots, *self.cache, self.turns)
+        return self.bq.lqmm_kv_append_norm(q, k, v, positions, slots, *self.cache, q_norm=self.q_norm,
+                                           k_norm=self.k_norm, eps=self.eps, rope_turns=self.turns)
+
+    def _attend(self, q, pages, lens, **kw):
+        call = self.bq.lqmm_attn_prefix if self.kv_bits == 16 else self.bq.lqmm_attn_prefix_f8
+        return call(q, *self.cache, pages, lens, **kw)
+
     def _output(self, o):
-        codes, scales = self.bq.lqmm_quant_f8b128(o.view(o.shape[0], -1))
-        return self.bq.lqmm_gemm_f8b128(self.wo, self.wo_scale, codes, scales)
+        return self._product(self.wo, self.wo_scale, o.view(o.shape[0], -1))
 
     def prompt(self, x):
         """Computes the shared prompt x (T, hidden) into its pages; returns the
@@ -85,11 +121,10 @@ class SharedPromptAttention:
         q, k, v = self._project(x)
         at = torch.arange(n, device=self.dev)
         slots = self.prompt_pages.long()[at // self.ps] * self.ps + at % self.ps
-        q = self.bq.lqmm_kv_append(q, k, v, at.int(), slots, self.k_cache, self.v_cache, self.turns)
+        q = self._append(q, k, v, at.int(), slots)
         i32 = dict(dtype=torch.int32, device=self.dev)
-        o = self.bq.lqmm_attn_prefix(q, self.k_cache, self.v_cache, self.prompt_pages[None],
-                                     torch.tensor([n], **i32), q_start=torch.tensor([0, n], **i32),
-                                     max_q=n)
+        o = self._attend(q, self.prompt_pages[None], torch.tensor([n], **i32),
+                         q_start=torch.tensor([0, n], **i32), max_q=n)
         self.prompt_len = n
         return self._output(o)
 
@@ -103,12 +138,29 @@ class SharedPromptAttention:
         n = self.lens.clamp(0, self.slots.shape[1] - 1)
         full = n == self.slots.shape[1] - 1
         slots = self.slots[self.rows, n]
-        q = self.bq.lqmm_kv_append(q, k, v, self.lens + self.prompt_len, slots, self.k_cache,
-                                   self.v_cache, self.turns)
+        q = self._append(q, k, v, self.lens + self.prompt_len, slots)
         self.torch.add(n, ~full, out=self.lens)
-        o = self.bq.lqmm_attn_prefix(q, self.k_cache, self.v_cache, self.pages, self.lens,
-                                     prefix_pages=self.prompt_pages, prefix_len=self.prompt_len)
+        o = self._attend(q, self.pages, self.lens, prefix_pages=self.prompt_pages,
+                         prefix_len=self.prompt_len)
         return self._output(o).masked_fill_(full[:, None], float("nan"))
+
+    def keys_values(self, dtype=None):
+        """What an 8-bit cache holds, as dense rows: (k, v, starts), rows starts[0]
+        .. starts[1] - 1 the shared prompt's and starts[1 + b] .. starts[2 + b] - 1
+        conversation b's own, keys as they were rotated. Waits for the lengths."""
+        if self.kv_bits != 8:
+            raise ValueError("keys_values reads an 8-bit cache")
+        torch = self.torch
+        counts = [self.prompt_len] + self.lens.tolist()
+        pages = torch.zeros(len(counts), max(self.prompt_pages.numel(), self.pages.shape[1]),
+                            dtype=torch.int32, device=self.dev)
+        pages[0, :self.prompt_pages.numel()] = self.prompt_pages
+        pages[1:, :self.pages.shape[1]] = self.pages
+        starts = np.concatenate(([0], np.cumsum(counts))).tolist()
+        k, v = self.bq.lqmm_kv_read_f8(*self.cache, pages,
+                                       torch.tensor(starts, dtype=torch.int32, device=self.dev),
+                                       starts[-1], dtype=dtype)
+        return k, v, starts
 
     def capture(self, x):
         """A HIP graph of one step that reads x; returns (graph, output). Steps
@@ -157,18 +209,23 @@ def main():
     g.manual_seed(0)
     wqkv = torch.randn((hq + 2 * hkv) * d, hidden, device="cuda", generator=g) / hidden ** 0.5
     wo = torch.randn(hidden, hq * d, device="cuda", generator=g) / hidden ** 0.5
-    layer = SharedPromptAttention(wqkv, wo, hq, hkv, d, batch, prompt_pages=512, max_pages=8)
-    layer.prompt(torch.randn(8000, hidden, device="cuda", generator=g).half())
+    xp = torch.randn(8000, hidden, device="cuda", generator=g).half()
     x = torch.randn(batch, hidden, device="cuda", generator=g).half()
-    graph, _ = layer.capture(x)
-    graph.replay()
-    torch.cuda.synchronize()
-    t, n = time.perf_counter(), 100
-    for _ in range(n):
+    ones = torch.ones(d, device="cuda")
+    for what, kw in (("e4m3 products, 16-bit cache", {}),
+                     ("4-bit products, 8-bit cache, norms of q and k",
+                      dict(weight_bits=4, kv_bits=8, q_norm=ones, k_norm=ones))):
+        layer = SharedPromptAttention(wqkv, wo, hq, hkv, d, batch, prompt_pages=512, max_pages=8, **kw)
+        layer.prompt(xp)
+        graph, _ = layer.capture(x)
         graph.replay()
-    torch.cuda.synchronize()
-    print(f"{batch} conversations behind 8000 tokens: {(time.perf_counter() - t) / n * 1e6:.1f} us "
-          f"per decode step of one attention block ({hidden} hidden, {hq}/{hkv} heads of {d})")
+        torch.cuda.synchronize()
+        t, n = time.perf_counter(), 100
+        for _ in range(n):
+            graph.replay()
+        torch.cuda.synchronize()
+        print(f"{batch} conversations behind 8000 tokens: {(time.perf_counter() - t) / n * 1e6:.1f} us "
+              f"per decode step of one attention block ({hidden} hidden, {hq}/{hkv} heads of {d}; {what})")
 
 
 if __name__ == "__main__":
