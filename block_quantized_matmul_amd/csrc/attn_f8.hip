@@ -35,6 +35,25 @@ __device__ __forceinline__ int64_t vector_at(const AttnPrefix &a, const Item &it
   return ((page * a.n_kv_heads + it.h) << a.page_log2) + (j & ((1 << a.page_log2) - 1));
 }
 
+// The item of a workgroup. Workgroups are handed to the 8 XCDs in turn, and each
+// has its own L2: the row blocks of a chunk and head, which read the same keys,
+// follow each other on one XCD, and chunks go to the XCDs in turn, the prefix's
+// and then the sequences', so that each XCD has its share of both and of the long
+// sequences (64 rows behind 16000 shared keys: 73 us when each XCD has the next
+// eighth of all items).
+__device__ __forceinline__ uint32_t dealt(uint32_t block, uint32_t n, uint32_t row_blocks) {
+  const uint32_t whole = n / (8 * row_blocks) * (8 * row_blocks), i = block / 8;
+  if (block >= whole) return whole + spread(block - whole, n - whole);
+  return (i / row_blocks * 8 + block % 8) * row_blocks + i % row_blocks;
+}
+
+__device__ __forceinline__ uint32_t item_of(const AttnPrefix &a, uint32_t item0, uint32_t block, uint32_t n) {
+  const uint32_t left = item0 < (uint32_t)a.prefix_items ? (uint32_t)a.prefix_items - item0 : 0;
+  const uint32_t pre = left < n ? left : n;
+  return item0 + (block < pre ? dealt(block, pre, a.prefix_row_blocks)
+                              : pre + dealt(block - pre, n - pre, a.suffix_row_blocks));
+}
+
 // ---- values behind a mask -------------------------------------------------------
 // As in attn_prefix.hip: a masked weight is 0, and 0 times a NaN code is NaN. O
 // is looked through for NaN behind the keys' loop, and rows of a block with such
@@ -398,7 +417,7 @@ __global__ void __launch_bounds__(kThreads, D <= 128 ? 2 : 1)
 attn_f8_rows16_kernel(AttnPrefixF8 a, uint32_t item0) {
   __shared__ Rows16<D, kThreads / 64> sm;
   Item it;
-  const uint32_t idx = item0 + spread(blockIdx.x, gridDim.x);
+  const uint32_t idx = item_of(a, item0, blockIdx.x, gridDim.x);
   rows_of_no_sequence<T, D>(a, idx, kThreads);
   if (find_item(a, idx, kRows, it))
     rows16_body<T, D, kThreads / 64>(a, it, sm);
@@ -443,7 +462,7 @@ __device__ __forceinline__ bool wave_again(uint32_t item0, int rows_per_block, i
   asm volatile("" : "+s"(args), "+s"(block));
   const AttnPrefixF8 &a = *reinterpret_cast<const AttnPrefixF8 *>(args);  // the kernel's first argument
   Item it;
-  if (!find_item(a, item0 + spread(block, gridDim.x), rows_per_block, it)) return false;
+  if (!find_item(a, item_of(a, item0, block, gridDim.x), rows_per_block, it)) return false;
   const int row0 = it.row0 + from;
   if (row0 >= it.rows || !edge_has_nan<D>(a, it, it.past + it.per_token * (row0 / a.group))) return false;
   const int end = row0 + n < it.rows ? row0 + n : it.rows;
@@ -891,7 +910,7 @@ __global__ void __launch_bounds__(64 * NW, wide_waves(D, NW, R))
 attn_f8_wide_kernel(AttnPrefixF8 a, uint32_t item0) {
   extern __shared__ __attribute__((aligned(16))) uint8_t smem[];
   Item it;
-  const uint32_t idx = item0 + spread(blockIdx.x, gridDim.x);
+  const uint32_t idx = item_of(a, item0, blockIdx.x, gridDim.x);
   rows_of_no_sequence<T, D>(a, idx, 64 * NW);
   if (find_item(a, idx, 32 * R * NW, it))
     wide_body<T, D, NW, R>(a, it, item0, smem);
@@ -922,13 +941,16 @@ attn_f8_join_kernel(AttnPrefix a, uint32_t first, int slots) {
   if (live) {
 #pragma unroll 4
     for (int p = slot; p < parts; p += slots) m = fmaxf(m, a.part_ml[p * nrows + row].x);
-    if (d == 0) top[group] = m;
   }
-  __syncthreads();
+  if (slots > 1) {
+    if (live && d == 0) top[group] = m;
+    __syncthreads();
+  }
   float l = 0.f;
   float4_t o = {0.f, 0.f, 0.f, 0.f};
   if (live) {
-    for (int i = group - slot; i < group - slot + slots; ++i) m = fmaxf(m, top[i]);
+    if (slots > 1)
+      for (int i = group - slot; i < group - slot + slots; ++i) m = fmaxf(m, top[i]);
 #pragma unroll 4
     for (int p = slot; p < parts; p += slots) {
       // of a part that sees no key nothing counts
@@ -940,10 +962,14 @@ attn_f8_join_kernel(AttnPrefix a, uint32_t first, int slots) {
 #pragma unroll
       for (int r = 0; r < 4; ++r) o[r] += w * (seen ? x[r] : 0.f);
     }
-    *reinterpret_cast<float4_t *>(&part[group][d]) = o;
-    if (d == 0) sum[group] = l;
   }
-  __syncthreads();
+  if (slots > 1) {
+    if (live) {
+      *reinterpret_cast<float4_t *>(&part[group][d]) = o;
+      if (d == 0) sum[group] = l;
+    }
+    __syncthreads();
+  }
   if (!live || slot) return;
   for (int i = 1; i < slots; ++i) {
     l += sum[group + i];
@@ -1002,9 +1028,14 @@ hipError_t launch(const AttnPrefixF8 &a, hipStream_t stream) {
     e = launch_items<T, D>(a, a.suffix_wide, a.prefix_items, a.suffix_items, stream);
   }
   if (e != hipSuccess || a.prefix_parts + a.suffix_parts == 1) return e;
+  // parts are shared out where a group a row would leave CUs empty (each has room
+  // for eight workgroups)
+  const int64_t rows = a.tokens * a.n_q_heads;
   int slots = 1;
-  while (slots < kJoinGroups<D> && 2 * slots <= a.prefix_parts + a.suffix_parts) slots *= 2;
-  const int64_t rows = a.tokens * a.n_q_heads, per = kJoinGroups<D> / slots;
+  while (slots < kJoinGroups<D> && 2 * slots <= a.prefix_parts + a.suffix_parts &&
+         rows * slots < kJoinGroups<D> * 2048ll)
+    slots *= 2;
+  const int64_t per = kJoinGroups<D> / slots;
   return launch_in_pieces((rows + per - 1) / per, kThreads, [&](uint32_t first, unsigned n) {
     hipLaunchKernelGGL((attn_f8_join_kernel<T, D>), dim3(n), dim3(kThreads), 0, stream, a, first, slots);
   });
@@ -1027,16 +1058,16 @@ hipError_t launch_dim(const AttnPrefixF8 &a, hipStream_t stream) {
 // 128 keys and at most kAttnMaxChunk.
 void attn_f8_plan(AttnPrefixF8 &a, int64_t max_suffix, int num_cus) {
   // Rows of a work item: 16, 128 or 256 (wide 0, 1, 2), the least of an estimate
-  // fitted to measured calls: a fixed time and one for each row block, key and
-  // head (ps), to which an item's start counts as some 250 keys. 16 rows read the
-  // cache again for every 16; the others wait longer for their tiles, of which a
-  // work item has eight or more if there are keys. Measured, 8 key heads, fp16
-  // (us; 16 / 128 / 256):
+  // fitted to measured calls: until the first results, which wait for up to 512
+  // or 768 keys, and then for each row block, key and head (ps), to which an
+  // item's start counts as 100 or 250 keys. 16 rows read the cache again for every
+  // 16. Measured, 8 key heads, fp16 (us; 16 / 128 / 256):
   // 128 dimensions, 60001 keys, 64 rows 59 / 80 / 79, 128 rows 99 / 83 / 85,
   // 256 rows 174 / 142 / 94; 16001 keys, 128 rows 30 / 35 / 34, 256 rows
   // 52 / 50 / 41; 4001 keys, 384 rows 29 / 38 / 36; 64 dimensions, 60001 keys,
   // 64 rows 35 / 51 / 59, 128 rows 59 / 53 / 61, 256 rows 102 / 91 / 65; 32 x 64
-  // keys, 128 rows each 18 / 14, 256 rows 30 / - / 17.
+  // keys, 128 rows each 18 / 14, 256 rows 30 / - / 17; 256 rows behind 8000 shared
+  // keys 32 / - / 39.
   auto wide_for = [&](int64_t rows, int64_t sequences, int64_t keys) {
     struct Cost {
       int rows16, rows128, rows256;
@@ -1045,11 +1076,12 @@ void attn_f8_plan(AttnPrefixF8 &a, int64_t max_suffix, int num_cus) {
                    : a.head_dim == 96 ? Cost{15, 120, 158}
                    : a.head_dim == 128 ? Cost{20, 130, 130}
                                        : Cost{47, 242, 0};
-    const double all = (double)sequences * a.n_kv_heads * (keys + 250);
-    const double tiles = 27e3 * (keys < 512 ? keys : 512);
-    const double few = 12e6 + c.rows16 * all * ((rows + 15) / 16);
-    const double mid = 6e6 + tiles + c.rows128 * all * ((rows + 127) / 128);
-    const double many = 16e6 + tiles + c.rows256 * all * ((rows + 255) / 256);
+    if (rows <= kRows) return 0;
+    const double heads = (double)sequences * a.n_kv_heads;
+    const auto until = [&](int most) { return 27e3 * (keys < most ? keys : most); };
+    const double few = 5e6 + until(512) / 2 + c.rows16 * heads * (keys + 250) * ((rows + 15) / 16);
+    const double mid = 6e6 + until(512) + c.rows128 * heads * (keys + 100) * ((rows + 127) / 128);
+    const double many = 10e6 + until(768) + c.rows256 * heads * (keys + 100) * ((rows + 255) / 256);
     if (c.rows256 && many < mid && many < few) return 2;
     return mid < few ? 1 : 0;
   };
