@@ -1028,12 +1028,12 @@ hipError_t launch(const AttnPrefixF8 &a, hipStream_t stream) {
     e = launch_items<T, D>(a, a.suffix_wide, a.prefix_items, a.suffix_items, stream);
   }
   if (e != hipSuccess || a.prefix_parts + a.suffix_parts == 1) return e;
-  // parts are shared out where a group a row would leave CUs empty (each has room
-  // for eight workgroups)
+  // parts are shared out where a group a row would leave CUs empty (each takes
+  // four workgroups)
   const int64_t rows = a.tokens * a.n_q_heads;
   int slots = 1;
   while (slots < kJoinGroups<D> && 2 * slots <= a.prefix_parts + a.suffix_parts &&
-         rows * slots < kJoinGroups<D> * 2048ll)
+         rows * slots < kJoinGroups<D> * 1024ll)
     slots *= 2;
   const int64_t per = kJoinGroups<D> / slots;
   return launch_in_pieces((rows + per - 1) / per, kThreads, [&](uint32_t first, unsigned n) {
