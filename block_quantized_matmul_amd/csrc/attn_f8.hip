@@ -436,14 +436,21 @@ constexpr float kSlack = 8.0f;
 template <class T>
 constexpr float kWideShift = kShift<T> - kSlack;
 
-// Waves of a SIMD that the wide kernel's registers leave room for.
+// Waves of a SIMD that the wide kernel's registers leave room for, keys of a tile,
+// and what a CU then holds: two workgroups, which wait at barriers of their own,
+// or one of eight waves (128 dimensions, 256 rows). Measured with 128 rows, 60001
+// keys, 8 key heads: 128 dimensions 74 us with two workgroups and tiles of 32
+// keys, 84 with one and 64; 64 dimensions 44 us with 64 keys, 57 with 32.
 constexpr int wide_waves(int d, int nw, int r) {
-  return r > 1 ? (d == 64 ? 2 : 1) : d <= 128 && nw == 8 ? 2 : 1;
+  return r > 1 ? (d == 64 ? 2 : 1) : d <= 128 ? 2 : 1;
+}
+constexpr int wide_keys(int d, int nw, int r) {
+  return d > 128 || (d > 64 && nw == 4 && r == 1) ? 32 : 64;
 }
 
-template <int D>
+template <int D, int KEYS>
 struct Wide {
-  static constexpr int kKeys = D <= 128 ? 64 : 32;  // keys of a tile
+  static constexpr int kKeys = KEYS;
   static constexpr int kHalf = kKeys * D * 2;       // bytes of a tile's K (and V)
   // a round is two tiles between barriers: K of it and of the tile after, V of
   // it, and the next round's two tiles of each on their way
@@ -475,7 +482,7 @@ __device__ __forceinline__ void wide_body(const AttnPrefixF8 &a, const Item &it,
                                           uint8_t *smem) {
   typedef typename T::elem elem;
   typedef typename T::vec8 vec8;
-  typedef Wide<D> C;
+  typedef Wide<D, wide_keys(D, NW, R)> C;
   constexpr int KT = C::kKeys;
   constexpr int kQ = D / 16;                     // k-steps of a logit tile
   constexpr int kDT = D / 32;                    // 32-wide tiles of O
@@ -990,10 +997,11 @@ attn_f8_join_kernel(AttnPrefix a, uint32_t first, int slots) {
 template <class T, int D, int NW, int R>
 hipError_t launch_wide(const AttnPrefixF8 &a, int64_t item0, int64_t items, hipStream_t stream) {
   constexpr auto kern = attn_f8_wide_kernel<T, D, NW, R>;
-  const hipError_t e = ensure_max_lds<kern>(Wide<D>::kLds);
+  constexpr int kLds = Wide<D, wide_keys(D, NW, R)>::kLds;
+  const hipError_t e = ensure_max_lds<kern>(kLds);
   if (e != hipSuccess) return e;
   return launch_in_pieces(items, 64 * NW, [&](uint32_t first, unsigned n) {
-    hipLaunchKernelGGL(kern, dim3(n), dim3(64 * NW), Wide<D>::kLds, stream, a, (uint32_t)item0 + first);
+    hipLaunchKernelGGL(kern, dim3(n), dim3(64 * NW), kLds, stream, a, (uint32_t)item0 + first);
   });
 }
 
@@ -1062,25 +1070,25 @@ void attn_f8_plan(AttnPrefixF8 &a, int64_t max_suffix, int num_cus) {
   // or 768 keys, and then for each row block, key and head (ps), to which an
   // item's start counts as 100 or 250 keys. 16 rows read the cache again for every
   // 16. Measured, 8 key heads, fp16 (us; 16 / 128 / 256):
-  // 128 dimensions, 60001 keys, 64 rows 59 / 80 / 79, 128 rows 99 / 83 / 85,
-  // 256 rows 174 / 142 / 94; 16001 keys, 128 rows 30 / 35 / 34, 256 rows
-  // 52 / 50 / 41; 4001 keys, 384 rows 29 / 38 / 36; 64 dimensions, 60001 keys,
-  // 64 rows 35 / 51 / 59, 128 rows 59 / 53 / 61, 256 rows 102 / 91 / 65; 32 x 64
-  // keys, 128 rows each 18 / 14, 256 rows 30 / - / 17; 256 rows behind 8000 shared
+  // 128 dimensions, 60001 keys, 64 rows 59 / 70 / 79, 128 rows 99 / 74 / 85,
+  // 256 rows 174 / 112 / 94; 16001 keys, 128 rows 30 / 37 / 34, 256 rows
+  // 52 / 46 / 41; 4001 keys, 384 rows 29 / 34 / 36; 64 dimensions, 60001 keys,
+  // 64 rows 35 / 42 / 56, 128 rows 59 / 44 / 58, 256 rows 102 / 64 / 65; 32 x 64
+  // keys, 128 rows each 18 / 13, 256 rows 30 / 17 / 17; 256 rows behind 8000 shared
   // keys 32 / - / 39.
   auto wide_for = [&](int64_t rows, int64_t sequences, int64_t keys) {
     struct Cost {
       int rows16, rows128, rows256;
     };
-    const Cost c = a.head_dim == 64   ? Cost{12, 83, 100}
-                   : a.head_dim == 96 ? Cost{15, 120, 158}
-                   : a.head_dim == 128 ? Cost{20, 130, 130}
+    const Cost c = a.head_dim == 64   ? Cost{12, 47, 62}
+                   : a.head_dim == 96 ? Cost{15, 80, 158}
+                   : a.head_dim == 128 ? Cost{20, 85, 130}
                                        : Cost{47, 242, 0};
     if (rows <= kRows) return 0;
     const double heads = (double)sequences * a.n_kv_heads;
     const auto until = [&](int most) { return 27e3 * (keys < most ? keys : most); };
     const double few = 5e6 + until(512) / 2 + c.rows16 * heads * (keys + 250) * ((rows + 15) / 16);
-    const double mid = 6e6 + until(512) + c.rows128 * heads * (keys + 100) * ((rows + 127) / 128);
+    const double mid = 8e6 + until(768) + c.rows128 * heads * (keys + 100) * ((rows + 127) / 128);
     const double many = 10e6 + until(768) + c.rows256 * heads * (keys + 100) * ((rows + 255) / 256);
     if (c.rows256 && many < mid && many < few) return 2;
     return mid < few ? 1 : 0;
@@ -1093,16 +1101,18 @@ void attn_f8_plan(AttnPrefixF8 &a, int64_t max_suffix, int num_cus) {
   // a sequence is cut, it is into chunks of at most 2048 keys: lengths differ, and
   // the call ends with the longest chunks (24 x 8209 ragged, 8 key heads: 52.8 us,
   // 59.5 with two chunks; 32 key heads 168, 230 with two; 64 x 12001, 8 key heads
-  // 170, 214 with two). Wide kernel: whole rounds over the CUs.
+  // 170, 214 with two). Wide kernel: whole rounds over what the CUs hold.
   auto chunk_of = [&](int64_t keys, int64_t blocks, int wide) {
     const int64_t most = (keys + 127) / 128;
     int64_t parts = (num_cus + blocks - 1) / blocks;
     if (wide) {
+      const int64_t room = (a.head_dim == 64 || (wide == 1 && a.head_dim <= 128) ? 2 : 1) * num_cus;
       int64_t best = -1;
       for (int64_t p = 1; p <= most && p <= 64; ++p) {
         const int64_t chunk = ((keys + p - 1) / p + 127) / 128 * 128;
-        // a workgroup's fixed cost is about that of 256 keys
-        const int64_t cost = (blocks * p + num_cus - 1) / num_cus * (chunk + 256);
+        // a workgroup's fixed cost is about that of 256 keys, and a part's, whose
+        // results are written and read once more, of blocks * head_dim / 96
+        const int64_t cost = (blocks * p + room - 1) / room * (chunk + 256) + p * blocks * a.head_dim / 96;
         if (best < 0 || cost < best) {
           best = cost;
           parts = p;
