@@ -151,6 +151,7 @@ kv_append_norm_kernel(KvAppendNorm a, uint32_t first) {
       }
       __syncthreads();
     }
+    if (h >= a.n_q_heads + a.n_kv_heads) return;  // whole vectors
     const float *weight = is_k ? a.k_norm : a.q_norm;
     if (weight) {
       normalize<L, D>(x, y, a.eps);
@@ -181,7 +182,7 @@ kv_append_norm_kernel(KvAppendNorm a, uint32_t first) {
       store8<TC>(dst + e1, y);
       return;
     }
-    if (slot < 0 || slot >= nslots || hk >= a.n_kv_heads) return;  // whole vectors
+    if (slot < 0 || slot >= nslots) return;
     const int64_t vec = (((slot >> a.page_log2) * a.n_kv_heads + hk) << a.page_log2) + (slot & in_page);
     if constexpr (F8) {
       const int b = vector_scale<L>(x, y, a.most_scale);
