@@ -9,6 +9,10 @@
 // device only: the groups of sequence b are numbered from starts[b] / 8 + b on,
 // which leaves room for each, and a workgroup finds its sequence by a search over
 // starts, 64 at a time.
+//
+// Bound by memory, mostly by what is written: 24 ragged sequences of up to 8209
+// tokens, 8 heads of 128, to bf16 127 us, which is the rate of a large copy (124).
+// 611 tokens 3.5 us: launch and three round trips, starts, page and codes.
 #include "f8_cache.hpp"
 #include "lqmm_internal.hpp"
 

@@ -37,7 +37,8 @@ typedef int i32x8 __attribute__((ext_vector_type(8)));
 constexpr int kQuantThreads = 256;
 
 // Four lanes take one block, eight values each: reads are 16 (32) bytes a lane
-// side by side, codes 4 bytes a lane.
+// side by side, codes 4 bytes a lane. 4096 x 4096 bf16 10.8 us (8.2 at the rate
+// of a large copy), 45 x 4128 fp32 2.7, one row of 8192 4 to 5: a launch.
 template <class T>
 __global__ void __launch_bounds__(kQuantThreads)
 quant_mxfp4_kernel(const typename T::elem *__restrict__ X, int64_t ldx, uint8_t *__restrict__ Xq,
