@@ -48,10 +48,13 @@ __device__ __forceinline__ int64_t vector_at(const AttnPrefix &a, const Item &it
 
 // The item of a workgroup. Workgroups are handed to the 8 XCDs in turn, and each
 // has its own L2: the row blocks of a chunk and head, which read the same keys,
-// follow each other on one XCD, and chunks go to the XCDs in turn, the prefix's
+// follow each other on one XCD, and heads go to the XCDs in turn, the prefix's
 // and then the sequences', so that each XCD has its share of both and of the long
 // sequences (64 rows behind 16000 shared keys: 73 us when each XCD has the next
-// eighth of all items).
+// eighth of all items, 46 so). All sequences' first chunks come before the second
+// ones, of which some hold nothing (24 sequences of 1000 keys under a page table
+// of 131072, 64 chunks: 145 us when a sequence's chunks go to the XCDs in turn,
+// 37 so).
 __device__ __forceinline__ uint32_t dealt(uint32_t block, uint32_t n, uint32_t row_blocks) {
   const uint32_t whole = n / (8 * row_blocks) * (8 * row_blocks), i = block / 8;
   if (block >= whole) return whole + spread(block - whole, n - whole);
@@ -61,8 +64,26 @@ __device__ __forceinline__ uint32_t dealt(uint32_t block, uint32_t n, uint32_t r
 __device__ __forceinline__ uint32_t item_of(const AttnPrefix &a, uint32_t item0, uint32_t block, uint32_t n) {
   const uint32_t left = item0 < (uint32_t)a.prefix_items ? (uint32_t)a.prefix_items - item0 : 0;
   const uint32_t pre = left < n ? left : n;
-  return item0 + (block < pre ? dealt(block, pre, a.prefix_row_blocks)
-                              : pre + dealt(block - pre, n - pre, a.suffix_row_blocks));
+  if (block < pre) return item0 + dealt(block, pre, a.prefix_row_blocks);
+  const uint32_t i = dealt(block - pre, n - pre, a.suffix_row_blocks);
+  if (n - pre != (uint32_t)a.suffix_items) return item0 + pre + i;  // (one of several launches)
+  const uint32_t unit = i / a.suffix_row_blocks, heads = (uint32_t)a.suffix_items / (a.suffix_row_blocks * a.suffix_parts);
+  const uint32_t chunk = unit / heads, head = unit - chunk * heads;
+  return (uint32_t)a.prefix_items + (head * a.suffix_parts + chunk) * a.suffix_row_blocks + i % a.suffix_row_blocks;
+}
+
+// An item without keys (page tables are wider than most sequences): the join is
+// told so, and reads nothing else of it (24 sequences of 1000 keys under a table of
+// 131072: 158 us with such items' sums stored and read as zeros, 145 so).
+__device__ __forceinline__ bool empty_item(const AttnPrefix &a, const Item &it, int rows_per_block, int threads) {
+  if (it.c0 < it.c1 || a.prefix_parts + a.suffix_parts == 1) return false;
+  const int G = a.group, end = it.rows - it.row0 < rows_per_block ? it.rows - it.row0 : rows_per_block;
+  for (int i = threadIdx.x; i < end; i += threads) {
+    const int row = it.row0 + i;
+    const int64_t flat = (it.tok0 + row / G) * a.n_q_heads + it.h * G + row % G;
+    a.part_ml[it.part * (a.tokens * a.n_q_heads) + flat] = make_float2(-INFINITY, 0.f);
+  }
+  return true;
 }
 
 // ---- values behind a mask -------------------------------------------------------
@@ -430,7 +451,7 @@ attn_f8_rows16_kernel(AttnPrefixF8 a, uint32_t item0) {
   Item it;
   const uint32_t idx = item_of(a, item0, blockIdx.x, gridDim.x);
   rows_of_no_sequence<T, D>(a, idx, kThreads);
-  if (find_item(a, idx, kRows, it))
+  if (find_item(a, idx, kRows, it) && !empty_item(a, it, kRows, kThreads))
     rows16_body<T, D, kThreads / 64>(a, it, sm);
 }
 
@@ -930,7 +951,7 @@ attn_f8_wide_kernel(AttnPrefixF8 a, uint32_t item0) {
   Item it;
   const uint32_t idx = item_of(a, item0, blockIdx.x, gridDim.x);
   rows_of_no_sequence<T, D>(a, idx, 64 * NW);
-  if (find_item(a, idx, 32 * R * NW, it))
+  if (find_item(a, idx, 32 * R * NW, it) && !empty_item(a, it, 32 * R * NW, 64 * NW))
     wide_body<T, D, NW, R>(a, it, item0, smem);
 }
 
@@ -956,9 +977,14 @@ attn_f8_join_kernel(AttnPrefix a, uint32_t first, int slots) {
   const bool live = group < kGroups && row < nrows;
   const int parts = a.prefix_parts + a.suffix_parts;
   float m = -INFINITY;
+  int end = 0;  // behind the last part that sees a key
   if (live) {
 #pragma unroll 4
-    for (int p = slot; p < parts; p += slots) m = fmaxf(m, a.part_ml[p * nrows + row].x);
+    for (int p = slot; p < parts; p += slots) {
+      const float2 ml = a.part_ml[p * nrows + row];
+      m = fmaxf(m, ml.x);
+      if (ml.y != 0.f) end = p + 1;
+    }
   }
   if (slots > 1) {
     if (live && d == 0) top[group] = m;
@@ -970,7 +996,7 @@ attn_f8_join_kernel(AttnPrefix a, uint32_t first, int slots) {
     if (slots > 1)
       for (int i = group - slot; i < group - slot + slots; ++i) m = fmaxf(m, top[i]);
 #pragma unroll 4
-    for (int p = slot; p < parts; p += slots) {
+    for (int p = slot; p < end; p += slots) {
       // of a part that sees no key nothing counts
       const float2 ml = a.part_ml[p * nrows + row];
       const float4_t x = *reinterpret_cast<const float4_t *>(a.part_o + (p * nrows + row) * D + d);
@@ -1108,11 +1134,13 @@ void attn_f8_plan(AttnPrefixF8 &a, int64_t max_suffix, int num_cus) {
   // give each CU a workgroup. With few blocks more chunks cost more at the join
   // than they gain (1 x 30001 keys, 8 key heads of 128 fp16: 18.6 us with one
   // workgroup a CU, 22 with two, 26 with four), with many one chunk a sequence is
-  // near the cache's read (64 x 8001 ragged: 108 us, 126 with two to four). Once
+  // near the cache's read (64 x 8001 ragged: 112 us, 126 with two to four). Once
   // a sequence is cut, it is into chunks of at most 2048 keys: lengths differ, and
-  // the call ends with the longest chunks (24 x 8209 ragged, 8 key heads: 52.8 us,
-  // 59.5 with two chunks; 32 key heads 168, 230 with two; 64 x 12001, 8 key heads
-  // 170, 214 with two). Wide kernel: whole rounds over what the CUs hold.
+  // the call ends with the longest chunks (24 x 8209 ragged, 8 key heads: 51 us,
+  // 60 with two chunks; 32 key heads 149, 172 with two; 64 x 12001, 8 key heads
+  // 150, 160 with two). That stops at 16 workgroups a CU, since a table may be much
+  // wider than the sequences (24 x 1000 keys under a table of 131072: 37 us with 64
+  // chunks, 19 with 21, 17 with 16; of 1024: 15.6). Wide kernel: whole rounds over what the CUs hold.
   auto chunk_of = [&](int64_t keys, int64_t blocks, int wide) {
     const int64_t most = (keys + 127) / 128;
     int64_t parts = (num_cus + blocks - 1) / blocks;
@@ -1131,7 +1159,8 @@ void attn_f8_plan(AttnPrefixF8 &a, int64_t max_suffix, int num_cus) {
       }
     }
     if (!wide && (parts > 1 || keys > kAttnMaxChunk)) {
-      const int64_t cut = (keys + 2047) / 2048;
+      int64_t cut = (keys + 2047) / 2048;
+      if (cut > 16ll * num_cus / blocks) cut = 16ll * num_cus / blocks;
       if (parts < cut) parts = cut;
     }
     if (parts > most) parts = most;

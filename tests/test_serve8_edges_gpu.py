@@ -279,3 +279,17 @@ def test_many_parts_give_the_rows_of_each_sequence_alone(hq, hkv, d, new, keys):
     sequence of one key, an empty one and rows of no sequence beside them."""
     b = Batch([keys, 1, 0], [new, 1, 1], hq, hkv, d, 16, 0, "f16", seed=keys)
     compare(*b.run(), b.want())
+
+
+@pytest.mark.parametrize("hq, hkv, d, new, prefix", [(8, 2, 128, 1, 0), (4, 4, 64, 1, 90), (4, 1, 256, 3, 0), (16, 1, 96, 40, 33)])
+def test_page_tables_wider_than_the_sequences(hq, hkv, d, new, prefix):
+    """Most chunks of the table's length hold nothing: against 64 bits, with an
+    empty sequence, and memory of the workspace that no part wrote is NaN."""
+    b = Batch([300, 1, 0, 129, 64], [new, 1, 1, new, 1], hq, hkv, d, 16, prefix, "f16", seed=31)
+    wide = np.full((5, 4096), -1, dtype=np.int32)
+    wide[:, :b.table.shape[1]] = b.table
+    b.table = wide
+    need = bq.lqmm_attn_prefix_f8_workspace_bytes(prefix, 4096, new, sum(b.news), 5, hq, hkv, d, 16)
+    assert need > 0
+    ws = torch.full((need,), 0xff, dtype=torch.uint8, device=DEV)
+    compare(*b.run(workspace=ws), b.want())
