@@ -63,7 +63,7 @@ class SharedPromptAttention:
         self.q_norm, self.k_norm = (
             None if w is None else w.to(device=self.dev, dtype=torch.float32).contiguous()
             for w in (q_norm, k_norm))
-        quantize = quantize_weight_f8b128 if weight_bits == 8 else bq.lqmm_quant_mxfp4
+        quantize = quantize_weight_f8b128 if weight_bits == 8 else self._quantize_weight_mxfp4
         self.wqkv, self.wqkv_scale = quantize(wqkv)
         self.wo, self.wo_scale = quantize(wo)
         # the cache: (k, v), in 8 bits (k, v, k_scales, v_scales)
@@ -87,6 +87,9 @@ class SharedPromptAttention:
         self.lens = torch.zeros(batch, **i32)
         self.prompt_len = 0
         self.rows = torch.arange(batch, device=self.dev)
+
+    def _quantize_weight_mxfp4(self, w):
+        return self.bq.lqmm_quant_mxfp4(w.float().contiguous())
 
     def _product(self, w, scale, x):
         if self.weight_bits == 4:
@@ -151,7 +154,8 @@ class SharedPromptAttention:
         if self.kv_bits != 8:
             raise ValueError("keys_values reads an 8-bit cache")
         torch = self.torch
-        counts = [self.prompt_len] + self.lens.tolist()
+        # (lengths as a step takes them)
+        counts = [self.prompt_len] + self.lens.clamp(0, self.slots.shape[1] - 1).tolist()
         pages = torch.zeros(len(counts), max(self.prompt_pages.numel(), self.pages.shape[1]),
                             dtype=torch.int32, device=self.dev)
         pages[0, :self.prompt_pages.numel()] = self.prompt_pages

@@ -126,3 +126,24 @@ def test_forms_that_are_not_there_are_refused(monkeypatch):
     layer, _ = block(monkeypatch)
     with pytest.raises(ValueError, match="8-bit"):
         layer.keys_values()
+
+
+def test_keys_values_takes_lengths_as_a_step_does(monkeypatch):
+    layer, calls = block(monkeypatch, kv_bits=8)
+    layer.prompt(torch.ones(3, 64))
+    layer.lens.copy_(torch.tensor([-7, 2 ** 31 - 1, 5], dtype=torch.int32))
+    assert layer.keys_values()[2] == [0, 3, 3, 19, 24]
+
+
+@pytest.mark.parametrize("change", [lambda w: w.double(), lambda w: w.t().contiguous().t(), lambda w: w.half()])
+def test_weights_are_taken_in_any_float_type_and_order(monkeypatch, change):
+    import block_quantized_matmul_amd as bq
+    from block_quantized_matmul_amd.serve import SharedPromptAttention
+    calls = Calls()
+    for name in dir(Calls):
+        if name.startswith(("_lqmm", "_kv")):
+            monkeypatch.setattr(bq, name[1:], getattr(calls, name[1:]))
+    w = [torch.randn(n, 64, generator=torch.Generator().manual_seed(n)).half().float() for n in (192, 64)]
+    SharedPromptAttention(change(w[0]), change(w[1]), 1, 1, 64, 2, 1, 1, weight_bits=4)
+    seen = [a[0] for n, a, _ in calls.seen if n == "lqmm_quant_mxfp4"]
+    assert len(seen) == 2 and all(s.is_contiguous() and s.dtype == torch.float32 and torch.equal(s, x) for s, x in zip(seen, w))
