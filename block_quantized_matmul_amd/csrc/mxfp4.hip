@@ -594,19 +594,20 @@ hipError_t launch_gemm(const uint8_t *W, const uint8_t *sw, const uint8_t *X, co
   // 4128 8.5 / 10.1 / 7.6 / 15.8 / 21.7 / 35; 64 x 4096 x 4096 11.3 / 7.2 / 8.6 /
   // 13.0 / 17.0 / 30; 128 x 14336 x 4096 65 / 42 / 43 / 19.0 / 19.3 / 31; 512 x
   // 14336 x 4096 245 / 163 / 145 / 57 / 36 / 38; 4096 x 14336 x 4096 - / - / - /
-  // 394 / 239 / 167.
+  // 394 / 239 / 167. 64 x 32 rows are for what then fits one round: 64 x 6144 x 4096
+  // 10.4 (32 x 32: 12.4), 64 x 14336 x 4096 20 (64 x 64: 14).
   struct Choice {
     int bm, bn, per_cu, fixed, piece;
   };
   constexpr Choice kChoices[] = {
       // straight to registers, K shared by eight waves
-      {16, 16, 2, 100, 520}, {32, 32, 1, 1000, 600}, {48, 32, 1, 1400, 700},
+      {16, 16, 2, 100, 520}, {32, 32, 1, 1000, 600}, {48, 32, 1, 1400, 700}, {64, 32, 1, 2600, 970},
       // LDS tiles: alone on a CU, or two on it
       {64, 64, 1, 3500, 1100}, {64, 64, 2, 4500, 1500}, {128, 128, 1, 3500, 1800}, {128, 128, 2, 1000, 4300},
       {256, 256, 1, 6000, 4350}};
   int best = -1;
   int64_t best_cost = 0;
-  for (int c = 0; c < 8; ++c) {
+  for (int c = 0; c < 9; ++c) {
     const Choice &o = kChoices[c];
     const int64_t tiles = ((M + o.bm - 1) / o.bm) * ((N + o.bn - 1) / o.bn);
     const int64_t slots = (int64_t)o.per_cu * num_cus;
@@ -621,11 +622,12 @@ hipError_t launch_gemm(const uint8_t *W, const uint8_t *sw, const uint8_t *X, co
     case 0: return launch_rows<T, 1, 1, 1, 8>(W, sw, X, sx, Y, M, N, K, stream);
     case 1: return launch_rows<T, 2, 2, 1, 8>(W, sw, X, sx, Y, M, N, K, stream);
     case 2: return launch_rows<T, 3, 2, 1, 8>(W, sw, X, sx, Y, M, N, K, stream);
-    case 3:
-    case 4: return launch_tile<T, 64, 64, 2, 2, 4>(W, sw, X, sx, Y, M, N, K, num_cus, stream);
-    case 5:
-    case 6: return launch_tile<T, 128, 128, 2, 4, 4>(W, sw, X, sx, Y, M, N, K, num_cus, stream);
-    case 7: return launch_tile<T, 256, 256, 4, 2, 4>(W, sw, X, sx, Y, M, N, K, num_cus, stream);
+    case 3: return launch_rows<T, 4, 2, 1, 8>(W, sw, X, sx, Y, M, N, K, stream);
+    case 4:
+    case 5: return launch_tile<T, 64, 64, 2, 2, 4>(W, sw, X, sx, Y, M, N, K, num_cus, stream);
+    case 6:
+    case 7: return launch_tile<T, 128, 128, 2, 4, 4>(W, sw, X, sx, Y, M, N, K, num_cus, stream);
+    case 8: return launch_tile<T, 256, 256, 4, 2, 4>(W, sw, X, sx, Y, M, N, K, num_cus, stream);
   }
   return hipErrorInvalidValue;
 }

@@ -293,3 +293,8 @@ def test_page_tables_wider_than_the_sequences(hq, hkv, d, new, prefix):
     assert need > 0
     ws = torch.full((need,), 0xff, dtype=torch.uint8, device=DEV)
     compare(*b.run(workspace=ws), b.want())
+
+
+@pytest.mark.parametrize("M, N, K", [(64, 6144, 4096), (50, 8100, 1056), (128, 4090, 2080), (61, 5001, 96)])
+def test_mx_products_of_sixty_four_rows(M, N, K):
+    check_mx(M, N, K, "bf16")
