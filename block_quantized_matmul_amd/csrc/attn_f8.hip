@@ -3,20 +3,23 @@
 //
 // Mathematics. With z_j = scale * log2(e) * q.k_j and V's values code_j 2^(e_j),
 //   O = sum_j 2^(z_j) 2^(e_j) code_j / sum_j 2^(z_j).
-// The exponents go to the logits: with y_j = z_j + e_j, any reference m and
-// w_j = 2^(y_j - m),
-//   O = sum_j w_j code_j / sum_j w_j 2^(-e_j).
-// m is kept near the largest y: the weights, which the matrix cores take in 16
-// bits, then lose nothing by scales that differ from token to token, and V's
-// codes are operands as they are. The scale of V costs no instruction at the
-// logits (the multiplication with scale * log2(e) becomes a multiply-add) and
-// none at the sum (an addition becomes one). K's scale costs none either: the
-// conversion of a lane's codes, all of one token, to 16 bits applies it.
-// A partial result is (m, sum w 2^-e, sum w code), joined as in attn_prefix.hip.
-// The kernel for many rows converts each code once for all of its rows, and V's
-// scales go with that in fp16 (the values are exact down to 2^-14, then in steps
-// of 2^-24); bf16 weights are multiplied by them instead, 2^(z_j) 2^(e_j) rounded
-// once. Its m is kept near the largest z.
+// bf16 has the range for it as it stands: with a reference m near the largest z
+// and w_j = 2^(z_j - m), the matrix cores take w_j 2^(e_j), rounded once, and V's
+// codes as they are, and the sum takes w_j.
+// fp16 has not. Few rows: the exponents go to the logits; with y_j = z_j + e_j, m
+// near the largest y and w_j = 2^(y_j - m),
+//   O = sum_j w_j code_j / sum_j w_j 2^(-e_j),
+// so that the weights lose nothing by scales that differ from token to token. The
+// scale of V costs no instruction at the logits (the multiplication with scale *
+// log2(e) becomes a multiply-add) and none at the sum (an addition becomes one).
+// (A w_j below 2^-126 is 0, also where 2^(-e_j) would make it count: the scales
+// have to lie closer together than fp32's exponents reach, as fp16's 2^67 do.)
+// Many rows: each code is converted once for all rows of a workgroup, V's with its
+// scale (the values are exact down to 2^-14, then in steps of 2^-24), and m is
+// near the largest z.
+// K's scale costs nothing: the conversion of a lane's codes, all of one token, to
+// 16 bits applies it. A partial result is (m, sum of weights, weighted sum) at m,
+// whichever it is, joined as in attn_prefix.hip.
 //
 // Bound (128 dimensions unless said): few rows by reading the cache, 24 ragged
 // sequences of up to 8209 keys, 8 key heads, 48 us and 5 for the join (floor 38);
@@ -203,6 +206,7 @@ __device__ __forceinline__ void rows16_body(const AttnPrefixF8 &a, const Item &i
   constexpr int kQ = D / 32;                       // 32-wide products of a logit tile
   constexpr int kDT = D / 16;                      // 16-wide tiles of O
   constexpr int kPass = Rows16<D, NW>::kPass;
+  constexpr bool kWithExponents = __is_same(T, TypeF16);  // V's exponents are in the logits
   static_assert(kDT % kPass == 0 && kPass % 2 == 0, "whole passes");
   int *ids = sm.ids;
 
@@ -306,14 +310,16 @@ __device__ __forceinline__ void rows16_body(const AttnPrefixF8 &a, const Item &i
     for (int i = 0; i < kDT / 2; ++i) v[i] = st.v[i];
     const u32x2 vs = st.vs;
     if (j0 + NW * kStep < it.c1) load(j0 + NW * kStep);
-    float y[2][4], back[2][4];  // logits with V's exponents; 2^-exponent
+    // logits; what a weight is multiplied by for the product with V (bf16), or for
+    // the sum beside logits with V's exponents (fp16)
+    float y[2][4], times[2][4];
 #pragma unroll
     for (int u = 0; u < 2; ++u)
 #pragma unroll
       for (int r = 0; r < 4; ++r) {
         const int b = (int)(vs[u] >> 8 * r & 255u);
-        y[u][r] = fmaf(s[u][r], a.scale_log2, (float)(b - 127));
-        back[u][r] = scale_inverse(b);
+        y[u][r] = kWithExponents ? fmaf(s[u][r], a.scale_log2, (float)(b - 127)) : s[u][r] * a.scale_log2;
+        times[u][r] = kWithExponents ? scale_inverse(b) : scale_of(b);
       }
     const int seen = limit < it.c1 ? limit : it.c1;
     if (j0 + kStep > it.c1 || j0 + kStep > all_see) {
@@ -323,7 +329,7 @@ __device__ __forceinline__ void rows16_body(const AttnPrefixF8 &a, const Item &i
         for (int r = 0; r < 4; ++r)
           if (j0 + 8 * g + 4 * u + r >= seen) {
             y[u][r] = -INFINITY;
-            back[u][r] = 0.f;  // (its byte may be anything)
+            times[u][r] = 0.f;  // (its byte may be anything)
           }
       // what lies behind the last key may be anything, and 0 * NaN is NaN
       if (j0 + kStep > it.c1) {
@@ -349,8 +355,8 @@ __device__ __forceinline__ void rows16_body(const AttnPrefixF8 &a, const Item &i
 #pragma unroll
       for (int r = 0; r < 4; ++r) {
         const float e = __builtin_amdgcn_exp2f(y[u][r] - ref);
-        l = fmaf(e, back[u][r], l);
-        p[4 * u + r] = (elem)e;
+        l = kWithExponents ? fmaf(e, times[u][r], l) : l + e;
+        p[4 * u + r] = (elem)(kWithExponents ? e : e * times[u][r]);
       }
 #pragma unroll
     for (int i = 0; i < kDT; ++i) {
