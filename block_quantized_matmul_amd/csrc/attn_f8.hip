@@ -13,7 +13,8 @@
 // scale of V costs no instruction at the logits (the multiplication with scale *
 // log2(e) becomes a multiply-add) and none at the sum (an addition becomes one).
 // (A w_j below 2^-126 is 0, also where 2^(-e_j) would make it count: the scales
-// have to lie closer together than fp32's exponents reach, as fp16's 2^67 do.)
+// have to lie closer together than fp32's exponents reach, as those that fp16
+// takes do, 2^67 apart.)
 // Many rows: each code is converted once for all rows of a workgroup, V's with its
 // scale (the values are exact down to 2^-14, then in steps of 2^-24), and m is
 // near the largest z.
@@ -40,6 +41,16 @@ namespace {
 template <class T>
 constexpr float kShift = __is_same(T, TypeF16) ? 14.0f : 0.0f;
 constexpr float kAloneShift = 0.0f;  // of rows done by themselves, in fp32
+
+// Scale bytes as they are taken. What fp16 holds ends at 2^7 times a code, and an
+// infinity would leave its row by the product with weights of 0 (a row whose mask
+// hides the key): larger scales, which only an append of bf16 writes, count as 2^7.
+// bf16: a byte of 254 or 255 beside a key that is not seen must be finite as well.
+template <class T>
+__device__ __forceinline__ uint32_t taken(uint32_t byte) {
+  constexpr uint32_t kMost = __is_same(T, TypeF16) ? kMostScaleF16 : 253;
+  return byte < kMost ? byte : kMost;
+}
 
 // First token vector of the group of eight that holds key j (in vectors of D
 // codes, of which each has one scale).
@@ -135,7 +146,7 @@ __device__ __forceinline__ void row_alone(const AttnPrefixF8 &a, const Item &it,
     float z = -INFINITY;
     if (j0 + lane < end) {
       const int64_t vec = vector_at(a, it, j0 + lane);
-      const float ks = scale_of(a.k_scales[vec]);
+      const float ks = scale_of(taken<T>(a.k_scales[vec]));
       float dot = 0.f;
 #pragma unroll 1
       for (int d = 0; d < D; d += 8) {
@@ -163,7 +174,7 @@ __device__ __forceinline__ void row_alone(const AttnPrefixF8 &a, const Item &it,
     for (int i = 0; i < n; ++i) {
       const int j = j0 + i;
       const int64_t vec = vector_at(a, it, j);
-      const float w = __shfl(e, i) * scale_of(a.v_scales[vec]);
+      const float w = __shfl(e, i) * scale_of(taken<T>(a.v_scales[vec]));
       const uint8_t *v = vc + (vec & ~7) * D + (vec & 7);
 #pragma unroll
       for (int u = 0; u < kO; ++u)
@@ -296,7 +307,7 @@ __device__ __forceinline__ void rows16_body(const AttnPrefixF8 &a, const Item &i
 #pragma unroll
     for (int u = 0; u < 2; ++u) {
       s[u] = float4_t{0.f, 0.f, 0.f, 0.f};
-      const float f = scale_of(st.ks[u]);
+      const float f = scale_of(taken<T>(st.ks[u]));
 #pragma unroll
       for (int i = 0; i < kK; ++i) {
         const u32x4 k = st.k[u][i];
@@ -317,7 +328,9 @@ __device__ __forceinline__ void rows16_body(const AttnPrefixF8 &a, const Item &i
     for (int u = 0; u < 2; ++u)
 #pragma unroll
       for (int r = 0; r < 4; ++r) {
-        const int b = (int)(vs[u] >> 8 * r & 255u);
+        // (what lies below 2^-60 is 0 in fp16's outputs, and its inverse too large for a sum)
+        int b = (int)taken<T>(vs[u] >> 8 * r & 255u);
+        if (kWithExponents && b < kLeastScale) b = kLeastScale;
         y[u][r] = kWithExponents ? fmaf(s[u][r], a.scale_log2, (float)(b - 127)) : s[u][r] * a.scale_log2;
         times[u][r] = kWithExponents ? scale_inverse(b) : scale_of(b);
       }
@@ -327,10 +340,7 @@ __device__ __forceinline__ void rows16_body(const AttnPrefixF8 &a, const Item &i
       for (int u = 0; u < 2; ++u)
 #pragma unroll
         for (int r = 0; r < 4; ++r)
-          if (j0 + 8 * g + 4 * u + r >= seen) {
-            y[u][r] = -INFINITY;
-            times[u][r] = 0.f;  // (its byte may be anything)
-          }
+          if (j0 + 8 * g + 4 * u + r >= seen) y[u][r] = -INFINITY;
       // what lies behind the last key may be anything, and 0 * NaN is NaN
       if (j0 + kStep > it.c1) {
         const int valid = it.c1 - (j0 + 8 * g);
@@ -644,14 +654,13 @@ __device__ __forceinline__ void wide_body(const AttnPrefixF8 &a, const Item &it,
       int g, u;
       if (!unit_of(i, g, u)) continue;
       const int key = 8 * (kGroups * wave + g) + u / (D / 16), chunk = 2 * (u % (D / 16));
-      const float f = scale_of(x.s[i]);
+      const float f = scale_of(taken<T>(x.s[i]));
       uint8_t *to = st + key * (2 * D);
       *reinterpret_cast<vec8 *>(to + 16 * (chunk ^ swz(key))) = values8<T>(u32x2{x.c[i][0], x.c[i][1]}, f);
       *reinterpret_cast<vec8 *>(to + 16 * ((chunk + 1) ^ swz(key))) = values8<T>(u32x2{x.c[i][2], x.c[i][3]}, f);
     }
   };
-  // A scale as it counts: a key that is not seen may have any byte beside its codes.
-  auto v_scale = [](uint32_t b) { return scale_of(b < 253u ? b : 253u); };
+  auto v_scale = [](uint32_t b) { return scale_of(taken<T>(b)); };
   auto store_v = [&](const VCodes &x, int tile) {
     uint8_t *st = v_stage(tile);
     const int j0 = it.c0 + tile * KT;

@@ -16,8 +16,9 @@
 namespace lqmm {
 
 constexpr float kCodeMax = 448.0f;  // largest e4m3 value, 1.75 * 2^8
-// Scales are 2^-60 .. 2^60 (fp16: .. 2^7, whose largest code stands for 57344):
-// a row of attention adds up to 2^13 weights divided by V's scales in fp32.
+// Scales are 2^-60 .. 2^60: sums of 2^13 values stay in fp32's range. In fp16 the
+// largest is 2^7, whose largest code stands for 57344; attention's 16-row kernel
+// divides weights by V's scales, and those lie 2^67 apart then.
 constexpr int kLeastScale = 127 - 60;
 constexpr int kMostScaleF16 = 127 + 7, kMostScaleBF16 = 127 + 60;
 

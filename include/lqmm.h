@@ -382,7 +382,8 @@ lqmm_status lqmm_quant_f8b128(const void *X, int x_type, int64_t ldx, uint8_t *X
  * type is fp16 (larger values are held as the largest code); its codes are x *
  * 2^-e to nearest even. An infinity or NaN is held as NaN and does not count for
  * e. Reading, bytes 1 to 253 are scales; what 0, 254 and 255 stand for is left
- * open, for the rows that see such a key.
+ * open, for the rows that see such a key. Which type a cache was written for is
+ * not kept with it: attention whose type is fp16 takes scales above 2^7 as 2^7.
  */
 
 /*
@@ -422,8 +423,10 @@ lqmm_status lqmm_kv_read_f8(const uint8_t *k_cache, const uint8_t *v_cache, cons
 /*
  * lqmm_attn_prefix over the 8-bit cache; `type` (fp16 or bf16) is that of q and
  * out. Keys and values enter the products exactly, but for fp16 values below
- * 2^-14, which may enter in steps of 2^-24. The rest is as for lqmm_attn_prefix, a
- * NaN code being a NaN value.
+ * 2^-14, which may enter in steps of 2^-24, and those of scales above 2^7, which
+ * enter as with 2^7 (below 65504). In bf16 a value times its weight is held down
+ * to 2^-126, and the sums hold values below 2^114. The rest is as for
+ * lqmm_attn_prefix, a NaN code being a NaN value.
  */
 lqmm_status lqmm_attn_prefix_f8(const void *q, int64_t ldq, const uint8_t *k_cache,
                                 const uint8_t *v_cache, const uint8_t *k_scales,

@@ -6,6 +6,7 @@ import pytest
 import block_quantized_matmul_amd as bq
 import serve_oracle as so
 from test_serve8_gpu import Batch, compare
+from test_serve8_wide_gpu import BEHIND, LONG, SHORT, Wide
 
 pytestmark = pytest.mark.gpu
 
@@ -75,7 +76,7 @@ def test_a_key_at_the_largest_scale_beside_keys_at_the_least(case):
     compare(*b.run(scale=LN2), b.want(LN2))
 
 
-@pytest.mark.parametrize("t", ["bf16"])
+@pytest.mark.parametrize("t", ["f16", "bf16"])
 @pytest.mark.parametrize("byte", [1, 11, 25, 66])
 @pytest.mark.parametrize("lens, news, hq, hkv, d", [([97], [1], 4, 2, 64), ([3000], [1], 2, 1, 128), ([80], [60], 2, 1, 128)])
 def test_least_scales_leave_the_sums_whole(t, byte, lens, news, hq, hkv, d):
@@ -86,6 +87,45 @@ def test_least_scales_leave_the_sums_whole(t, byte, lens, news, hq, hkv, d):
     b.cache[3][b.cache[3] != 255] = byte
     wo, wl, bo, bl = b.want()
     compare(*b.run(), (wo, wl, bo + max(lens) * 448 * 2.0 ** -126, bl))
+
+
+HIDDEN = [([90], [70], 2, 2, 96, 0), ([80], [60], 2, 1, 256, 50), ([150], [140], 2, 1, 128, 0),
+          ([400, 390], [200, 390], 2, 1, 128, 200), ([300], [300], 2, 1, 64, 40), ([41, 33], [3, 2], 4, 2, 64, 0)]
+HIDDEN += [(*c[:4], d, c[4]) for c, d in ((SHORT, 64), (SHORT, 96), (SHORT, 256), (LONG, 64), (LONG, 128), (BEHIND, 128))]
+
+
+@pytest.mark.parametrize("t", ["f16", "bf16"])
+@pytest.mark.parametrize("byte", [0, 135, 200, 253, 254, 255])
+@pytest.mark.parametrize("what", ["k", "v"])
+@pytest.mark.parametrize("case", HIDDEN)
+def test_a_scale_past_the_type_stays_behind_the_mask(case, what, byte, t):
+    """The last new token has a scale past fp16's values, or a byte that stands for
+    nothing: the rows before it, whose mask leaves it out, are as without it."""
+    lens, news, hq, hkv, d, prefix = case
+    b = Wide(lens, news, hq, hkv, d, 16, prefix, t, seed=sum(lens))
+    want = b.want()
+    last = len(lens) - 1
+    p, o = slot_of(b, last, lens[last] - 1)
+    b.cache[2 if what == "k" else 3][p, :, o] = byte
+    out, lse = b.run()
+    rows = np.arange(sum(news)) != b.start[last + 1] - 1
+    compare(out[rows], lse[rows], [w[rows] for w in want])
+
+
+@pytest.mark.parametrize("case", HIDDEN + [([97, 5], [1, 1], 4, 2, 128, 0), ([300], [1], 2, 1, 64, 40)])
+@pytest.mark.parametrize("byte", [135, 140, 187, 253])
+def test_fp16_takes_larger_scales_as_its_largest(case, byte):
+    """A bf16 call's cache under fp16 queries: scales past 2^7 count as 2^7."""
+    lens, news, hq, hkv, d, prefix = case
+    b = Wide(lens, news, hq, hkv, d, 16, prefix, "f16", seed=sum(lens) + 1)
+    b.q *= 2.0 ** -14  # (logits stay ordinary)
+    r = np.random.default_rng(byte)
+    for c in b.cache[2:]:
+        c[(c != 255) & (r.random(c.shape) < 0.2)] = byte
+    got = b.run()
+    for c in b.cache[2:]:
+        c[(c > 134) & (c != 255)] = 134
+    compare(*got, b.want())
 
 
 def test_attention_repeats_itself():
