@@ -161,6 +161,9 @@ class SharedPromptAttention:
         pages[0, :self.prompt_pages.numel()] = self.prompt_pages
         pages[1:, :self.pages.shape[1]] = self.pages
         starts = np.concatenate(([0], np.cumsum(counts))).tolist()
+        if starts[-1] == 0:  # nothing held yet
+            k, v = torch.empty(2, 0, self.hkv, self.d, dtype=dtype or torch.float16, device=self.dev)
+            return k, v, starts
         k, v = self.bq.lqmm_kv_read_f8(*self.cache, pages,
                                        torch.tensor(starts, dtype=torch.int32, device=self.dev),
                                        starts[-1], dtype=dtype)
