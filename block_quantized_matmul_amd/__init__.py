@@ -529,15 +529,17 @@ def lqmm_gemm_f8b128(W, wscale, Xq, xscale, out=None, out_dtype=None, stream=Non
 
 def lqmm_kv_append_norm(q, k, v, positions, slots, k_cache, v_cache, k_scales=None, v_scales=None,
                         q_norm=None, k_norm=None, eps=1e-6, rope_turns=None, interleaved=False,
-                        q_out=None, stream=None):
+                        q_out=None, stream=None, dtype=None):
     """lqmm_kv_append with norms: each head of q and k becomes x / sqrt(mean(x^2)
     + eps) * weight (q_norm, k_norm: float32 (head_dim,), None: no norm) before
     the rotation. The caches are float16 or bfloat16, or 8-bit codes with
-    k_scales and v_scales (num_pages, n_kv_heads, page_size). Returns the
-    rotated q in the 16-bit caches' type; with 8-bit caches in q_out's, else in
-    k's when that is 16-bit, else float16 (None without q)."""
+    k_scales and v_scales (num_pages, n_kv_heads, page_size). dtype: float16 or
+    bfloat16, the type of the queries that an 8-bit cache is written for, which
+    bounds its scales (2^7 for float16), also where no q is given; None: q_out's,
+    else k's when that is 16-bit, else float16. Returns the rotated q in it, or in
+    the 16-bit caches' type (None without q)."""
     return _calls().kv_append_norm(q, k, v, positions, slots, k_cache, v_cache, k_scales, v_scales,
-                                   q_norm, k_norm, eps, rope_turns, interleaved, q_out, stream)
+                                   q_norm, k_norm, eps, rope_turns, interleaved, q_out, stream, dtype)
 
 
 def lqmm_kv_read_f8(k_cache, v_cache, k_scales, v_scales, pages, starts, tokens, dtype=None,

@@ -206,9 +206,14 @@ bool arity(Py_ssize_t n, Py_ssize_t want) {
   return false;
 }
 
+at::ScalarType dtype_of(PyObject *o, const char *name) {
+  if (!THPDtype_Check(o)) type_error("%s must be a torch.dtype", name);
+  return reinterpret_cast<THPDtype *>(o)->scalar_type;
+}
+
 // What an append with norms takes beside lqmm_kv_append's arguments.
 struct Norms {
-  PyObject *k_scales, *v_scales, *q_norm, *k_norm, *eps;
+  PyObject *k_scales, *v_scales, *q_norm, *k_norm, *eps, *dtype;
 };
 
 const float *norm_weight(PyObject *o, const at::Tensor &like, int64_t dim, const char *name) {
@@ -270,9 +275,17 @@ PyObject *append(PyObject *const *a, const Norms *norms) {
       eps = PyFloat_AsDouble(norms->eps);
       if (eps == -1.0 && PyErr_Occurred()) throw Failed();
     }
-    // the type of q_out: the 16-bit caches'; beside 8-bit ones its own, or k's
+    // the type of q_out, and of an 8-bit cache's readers: the 16-bit caches'; beside
+    // 8-bit ones as asked for, or q_out's, or k's
     at::ScalarType q_type = f8 ? (type == LQMM_F32 ? at::kHalf : k.scalar_type()) : c.k.scalar_type();
-    if (f8 && out_o != Py_None) q_type = tensor(out_o, "q_out").scalar_type();
+    if (norms && norms->dtype != Py_None) {
+      const at::ScalarType asked = dtype_of(norms->dtype, "dtype");
+      if (f8 ? asked != at::kHalf && asked != at::kBFloat16 : asked != q_type)
+        type_error("%s must be float16 or bfloat16, and 16-bit caches' own", "dtype");
+      q_type = asked;
+    } else if (f8 && out_o != Py_None) {
+      q_type = tensor(out_o, "q_out").scalar_type();
+    }
     const c10::DeviceGuard guard(k.device());
     int64_t heads = 0, ldq = 0;
     const void *qp = nullptr;
@@ -327,10 +340,10 @@ PyObject *kv_append(PyObject *, PyObject *const *a, Py_ssize_t n) {
 }
 
 PyObject *kv_append_norm(PyObject *, PyObject *const *a, Py_ssize_t n) {
-  if (!arity(n, 16)) return nullptr;
+  if (!arity(n, 17)) return nullptr;
   // (a norm's arguments stand between the caches and the rotation's table)
   PyObject *plain[11] = {a[0], a[1], a[2], a[3], a[4], a[5], a[6], a[12], a[13], a[14], a[15]};
-  const Norms norms = {a[7], a[8], a[9], a[10], a[11]};
+  const Norms norms = {a[7], a[8], a[9], a[10], a[11], a[16]};
   return append(plain, &norms);
 }
 
@@ -345,10 +358,7 @@ PyObject *both_of(const at::Tensor &a, const at::Tensor &b) {
 
 // A torch.dtype argument, or the given output's type, or float16.
 at::ScalarType out_type(PyObject *dtype, PyObject *out, const char *name) {
-  if (dtype != Py_None) {
-    if (!THPDtype_Check(dtype)) type_error("%s must be a torch.dtype", name);
-    return reinterpret_cast<THPDtype *>(dtype)->scalar_type;
-  }
+  if (dtype != Py_None) return dtype_of(dtype, name);
   return out != Py_None ? tensor(out, "out").scalar_type() : at::kHalf;
 }
 
