@@ -563,8 +563,8 @@ def lqmm_attn_prefix_f8(q, k_cache, v_cache, k_scales, v_scales, pages, seq_lens
                         prefix_len=0, q_start=None, max_q=1, scale=None, out=None, return_lse=False,
                         lse=None, workspace=None, stream=None):
     """lqmm_attn_prefix over an 8-bit cache (float8_e4m3fn codes with a scale for
-    each token and head); q and out are float16 or bfloat16. workspace: of
-    lqmm_attn_prefix_f8_workspace_bytes."""
+    each token and head); q and out are float16 or bfloat16 (float16 takes scales
+    above 2^7 as 2^7). workspace: of lqmm_attn_prefix_f8_workspace_bytes."""
     return _calls().attn_prefix_f8(q, k_cache, v_cache, k_scales, v_scales, pages, seq_lens,
                                    prefix_pages, prefix_len, q_start, max_q, scale, out, return_lse,
                                    lse, workspace, stream)

@@ -1,6 +1,7 @@
 // What the attention kernels over a paged cache share (attn_prefix.hip,
-// attn_f8.hip): work items, rows of no sequence, and the join of partial
-// results. Included into an unnamed namespace's users; gfx950 only.
+// attn_f8.hip): work items, rows of no sequence, how partial results are weighed
+// when they are joined, and the join of attn_prefix.hip. All in an unnamed
+// namespace; gfx950 only.
 #pragma once
 
 #include "lqmm_internal.hpp"

@@ -25,9 +25,9 @@
 // Bound (128 dimensions unless said): few rows by reading the cache, 24 ragged
 // sequences of up to 8209 keys, 8 key heads, 48 us and 5 for the join (floor 38);
 // what is left is the end, where the longest chunks run alone. Many rows by the
-// vector ALU (54 % of the cycles, 75 % with 64 dimensions) and the matrix cores
+// vector ALU (54 % of the cycles, 76 % with 64 dimensions) and the matrix cores
 // (43 %, 33 %), mostly in turn: 96 x 8 rows a key head behind 32801 keys, bf16,
-// 137 us; 6 x 301 new tokens behind 8200 keys, 64 dimensions, fp16 168 us.
+// 132 us; 6 x 301 new tokens behind 8200 keys, 64 dimensions, fp16 163 us.
 //
 // Weights are held at 2^14 in fp16, as there; in bf16 at 1 (values are below 2^69,
 // so that no sum of a work item's 2^13 keys comes near the largest number).

@@ -16,10 +16,10 @@
 // adjacent and a token's scale is known only behind its whole vector.
 //
 // Bound by memory from some thousand tokens on: 16381 tokens, 64/8 heads of 128,
-// bf16 into 8 bits 133 us (124 at the rate of a large copy; the vector ALU is
-// busy two thirds of the time, with norms, turns and codes). 203 tokens, 40/8
-// heads, fp32 into 16 bits 6.8 us: half a token's heads are one workgroup's round
-// trip, V's lines are written in part. 1 token 3.6 us: launch and two dependent
+// bf16 into 8 bits 130 us (124 at the rate of a large copy; the vector ALU is
+// busy 60 % of the time, with norms, turns and codes). 203 tokens, 40/8
+// heads, fp32 into 16 bits 7.1 us: half a token's heads are one workgroup's round
+// trip, V's lines are written in part. 1 token 3.9 us: launch and two dependent
 // round trips.
 #include "f8_cache.hpp"
 #include "lqmm_internal.hpp"

@@ -11,7 +11,7 @@
 // starts, 64 at a time.
 //
 // Bound by memory, mostly by what is written: 24 ragged sequences of up to 8209
-// tokens, 8 heads of 128, to bf16 127 us, which is the rate of a large copy (124).
+// tokens, 8 heads of 128, to bf16 129 us, which is the rate of a large copy (124).
 // 611 tokens 3.5 us: launch and three round trips, starts, page and codes.
 #include "f8_cache.hpp"
 #include "lqmm_internal.hpp"

@@ -19,10 +19,12 @@
 // cores: LDS tiles and v_mfma_scale_f32_32x32x64_f8f6f4, which alone reach 7.8
 // PFLOP/s where the 16 x 16 x 128 form reaches 4.7 (one wave a SIMD) or 6; on
 // random codes, whose power draw lowers the clock, 5.3. 4096 x 14336 x 4096 runs
-// at 2.9 PFLOP/s (167 us; the vendor library 3.0 at 8192^3). Of that, measured on
-// timing copies, products 88 us, LDS reads 20, loads 30, scales 15, outputs 20: one
-// wave's instructions go out in turn, and the barrier of a step puts the two waves
-// of a SIMD in step, so that these overlap in part only.
+// at 2.9 to 3.2 PFLOP/s (152 to 163 us, by card; the vendor library 3.0 at
+// 8192^3). Of that, measured on timing copies, products 88 us, LDS reads 20, loads
+// 30, scales 15, outputs 20: one wave's instructions go out in turn, and the barrier
+// of a step puts the two waves of a SIMD in step, so that these overlap in part
+// only. From 16 to 1000 rows it stands 1.5 to 5 times above its floor: 19 to 39
+// bytes of W and X per ns come into a CU, too few are on their way.
 #include <type_traits>
 
 #include "lqmm_internal.hpp"
@@ -37,8 +39,8 @@ typedef int i32x8 __attribute__((ext_vector_type(8)));
 constexpr int kQuantThreads = 256;
 
 // Four lanes take one block, eight values each: reads are 16 (32) bytes a lane
-// side by side, codes 4 bytes a lane. 4096 x 4096 bf16 10.8 us (8.2 at the rate
-// of a large copy), 45 x 4128 fp32 2.7, one row of 8192 4 to 5: a launch.
+// side by side, codes 4 bytes a lane. 4096 x 4096 bf16 10.3 us (8.2 at the rate
+// of a large copy), 45 x 4128 fp32 2.2, one row of 8192 4 to 5: a launch.
 template <class T>
 __global__ void __launch_bounds__(kQuantThreads)
 quant_mxfp4_kernel(const typename T::elem *__restrict__ X, int64_t ldx, uint8_t *__restrict__ Xq,
